@@ -302,6 +302,102 @@ DIT_API int dit_joint_attention_e4m3(const uint8_t* q8, const uint8_t* k8, const
  * fmt (BF16 or F16).  out: [batch, S, d] in the same format. */
 DIT_API int dit_joint_attention(const void* qkv, void* out, int fmt, int batch, int seq, int n_heads, int head_dim, void* stream);
 
+/* ---- the training pass through the attention sublayer ----
+ * Gradients of the kernels above for fine-tuning on the frozen FP8 model (the pages train LoRA
+ * adapters on it: SimpleTuner Ideogram 4 quickstart, "LoRA と LyCORIS"), and the two forward forms
+ * that keep what the gradients need.  In order of use:
+ *   dit_qknorm_mrope_out        raw q, k of the fused qkv buffer -> rotated q, k in a second buffer
+ *   dit_joint_attention_lse     attention output and the log-sum-exp of every row
+ *   dit_joint_attention_backward  gradients of the rotated q and k, and of v
+ *   dit_qknorm_mrope_backward   gradients of the raw q and k, and of the two gains
+ *   dit_rmsnorm_rows_backward   gradient through the pre-norm, the residual's added, and of its gain
+ * (the products with the frozen weights are dit_gemm_w8a16 on transposed codes).
+ *
+ * Row views: a pointer with a leading dimension ld (elements) is a 16-bit [batch, seq, cols] view
+ * whose rows are ld apart and whose batch elements are seq * ld apart; ld >= cols, ld % 8 == 0,
+ * 16-byte aligned.  q and k inside [B, S, 2d], v inside the fused [B, S, 3d], and the gradients
+ * inside one [B, S, 3d] buffer are such views.
+ * Padded batches: key_lens (DEVICE int32 [batch], clamped to [0, seq]; NULL: all rows) gives the
+ * leading rows of each element that take part, as queries and as keys.  The rows behind them are
+ * never used, whatever they hold (NaN included); their outputs and gradients are written as zeros.
+ * Results do not depend on the order in which CTAs run: equal inputs give equal bits.
+ * Each call uses its workspace until its kernels have finished; calls that may overlap (other
+ * streams, captured graphs) need workspaces of their own. */
+
+/* dit_qknorm_mrope, out of place: the raw q and k (columns [0, 2d) of qkv [batch, S, 3d], fmt BF16
+ * or F16) stay as they are and the normalised, rotated ones go to qk [batch, S, 2d].
+ * text_lens: DEVICE int32 [batch] or NULL; as in dit_block_forward_padded (each element's own
+ *   positions; padding rows are computed like any row, at (0, 0, 0)).  Not together with pos.
+ * key_lens: optional DEVICE int32 [batch], receives each element's token count (L_b + grid_h *
+ *   grid_w, or S without text_lens).
+ * Other arguments and errors as dit_qknorm_mrope; INVALID_ARG for qk == qkv. */
+DIT_API int dit_qknorm_mrope_out(const void* qkv, void* qk, int fmt, int batch, int n_text, int grid_h, int grid_w,
+                                 int t_img, const int32_t* pos, const int32_t* text_lens, int32_t* key_lens,
+                                 const dit_block_config* cfg, const void* g_q, const void* g_k, void* stream);
+
+/* Bytes of device workspace dit_qknorm_mrope_backward needs (one partial row of gain sums per CTA). */
+DIT_API size_t dit_qknorm_mrope_backward_workspace_bytes(const dit_block_config* cfg, int batch, int seq);
+
+/* The gradient of dit_qknorm_mrope(_out).  Per head vector x of the raw q (or k), with
+ * r = 1 / sqrt(mean(x^2) + eps), xh = r x and R the token's rotation: dz = R^T dy,
+ * dg = sum dz xh over all tokens and heads, dx = r (dz g - xh mean(dz g xh)).
+ * qkv: the raw buffer the forward read.  dqk: row view of 2d columns, the gradients of the rotated
+ * q and k; dx: row view of 2d columns, receives those of the raw q and k (may be dqk itself, with
+ * the same ld).  Both in qkv's fmt.  dg_q, dg_k: fp32 [head_dim], overwritten.
+ * With text_lens the rows behind an element's L_b + grid_h * grid_w tokens get zeros and do not
+ * enter the gains' sums.  fp32 math.
+ * Errors: as dit_qknorm_mrope_out, WORKSPACE. */
+DIT_API int dit_qknorm_mrope_backward(const void* qkv, const void* dqk, int64_t ld_dqk, void* dx, int64_t ld_dx,
+                                      float* dg_q, float* dg_k, int fmt, int batch, int n_text, int grid_h, int grid_w,
+                                      int t_img, const int32_t* pos, const int32_t* text_lens,
+                                      const dit_block_config* cfg, const void* g_q, const void* g_k, void* workspace,
+                                      size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace dit_joint_attention_lse needs when key_lens is given. */
+DIT_API size_t dit_joint_attention_lse_workspace_bytes(int batch, int seq, int n_heads, int head_dim);
+
+/* dit_joint_attention on separate row views of q, k and v (d = n_heads * head_dim columns each),
+ * which also writes what its gradient needs:
+ *   out[b, i] = softmax(q_i k^T / sqrt(hd)) v per head,  lse[b, h, i] = log sum_j exp(q_i k_j / sqrt(hd))
+ * out: [batch, seq, d] in fmt (BF16 or F16); lse: fp32 [batch, n_heads, seq].  P is rounded to fmt
+ * for the product with v; the row sums are fp32.  workspace may be NULL when key_lens is.
+ * Errors: INVALID_ARG (also for out aliasing an input), UNSUPPORTED (head_dim), WORKSPACE. */
+DIT_API int dit_joint_attention_lse(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                                    int64_t ld_v, void* out, float* lse, int fmt, int batch, int seq, int n_heads,
+                                    int head_dim, const int32_t* key_lens, void* workspace, size_t ws_bytes,
+                                    void* stream);
+
+/* Bytes of device workspace dit_joint_attention_backward needs. */
+DIT_API size_t dit_joint_attention_backward_workspace_bytes(int batch, int seq, int n_heads, int head_dim);
+
+/* The gradient of dit_joint_attention_lse, the probabilities recomputed from q, k and lse:
+ *   P = exp(q k^T / sqrt(hd) - lse), dP = dout v^T, delta = rowsum(dout out),
+ *   dS = P (dP - delta) / sqrt(hd), dq = dS k, dk = dS^T q, dv = P^T dout.
+ * out, lse: as the forward wrote them; dout: [batch, seq, d] in fmt; dq, dk, dv: row views of d
+ * columns in fmt, no overlap with an input.  P and dS are rounded to fmt for the products (in F16
+ * under a power-of-two scale taken from the data, so small gradients do not vanish below f16's
+ * range); every sum is fp32.
+ * Errors: as dit_joint_attention_lse; WORKSPACE (always needed). */
+DIT_API int dit_joint_attention_backward(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
+                                         int64_t ld_v, const void* out, const void* dout, const float* lse, void* dq,
+                                         int64_t ld_dq, void* dk, int64_t ld_dk, void* dv, int64_t ld_dv, int fmt,
+                                         int batch, int seq, int n_heads, int head_dim, const int32_t* key_lens,
+                                         void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of device workspace dit_rmsnorm_rows_backward needs. */
+DIT_API size_t dit_rmsnorm_rows_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/* The gradient of dit_rmsnorm_rows, with r = 1 / sqrt(mean(x^2) + eps) per row:
+ *   dg = sum over rows of dy x r,   dx = r (dy g - x r^2 mean(dy g x)) + dres
+ * x: [rows, cols] in x_fmt (BF16 or F32); g: bf16 [cols]; dy: the gradient of y, in dy_fmt (BF16,
+ * F16 or F32); dres: optional gradient that reaches x past the norm (the residual), in dx_fmt, NULL
+ * for none; dx: [rows, cols] in dx_fmt (BF16, F16 or F32), may be dres itself; dg: fp32 [cols],
+ * overwritten (zeros for rows = 0).  fp32 math.
+ * Errors: INVALID_ARG (cols % 8, dx aliasing x or dy), UNSUPPORTED (cols > 8192), WORKSPACE. */
+DIT_API int dit_rmsnorm_rows_backward(const void* x, int x_fmt, const void* g, const void* dy, int dy_fmt,
+                                      const void* dres, void* dx, int dx_fmt, float* dg, int64_t rows, int64_t cols,
+                                      float eps, void* workspace, size_t ws_bytes, void* stream);
+
 /* Synchronise `stream`, then report (and clear) device-side errors recorded by any
  * kernel of this library on the current device since the last poll. */
 DIT_API int dit_poll_error(void* stream);

@@ -96,6 +96,18 @@ SIGNATURES = {
     "dit_qknorm_mrope_e4m3": (_I, [_P, _I, _I, _I, _I, _I, _I, _P, ctypes.POINTER(BlockConfig), _P, _P, _P, _P, _P,
                                    _P]),
     "dit_joint_attention_e4m3": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "dit_qknorm_mrope_out": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, ctypes.POINTER(BlockConfig), _P, _P,
+                                  _P]),
+    "dit_qknorm_mrope_backward_workspace_bytes": (_SZ, [ctypes.POINTER(BlockConfig), _I, _I]),
+    "dit_qknorm_mrope_backward": (_I, [_P, _P, _I64, _P, _I64, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P,
+                                       ctypes.POINTER(BlockConfig), _P, _P, _P, _SZ, _P]),
+    "dit_joint_attention_lse_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "dit_joint_attention_lse": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
+    "dit_joint_attention_backward_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "dit_joint_attention_backward": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P, _I64, _I,
+                                          _I, _I, _I, _I, _P, _P, _SZ, _P]),
+    "dit_rmsnorm_rows_backward_workspace_bytes": (_SZ, [_I64, _I64]),
+    "dit_rmsnorm_rows_backward": (_I, [_P, _I, _P, _P, _I, _P, _P, _I, _P, _I64, _I64, _F, _P, _SZ, _P]),
     "dit_poll_error": (_I, [_P]),
     "dit_profile_enable": (_I, [_I]),
     "dit_profile_enable_tags": (_I, [_I, ctypes.c_uint32]),
@@ -355,6 +367,165 @@ def joint_attention_e4m3(q8: torch.Tensor, k8: torch.Tensor, scale: torch.Tensor
     _check("dit_joint_attention_e4m3", lib().dit_joint_attention_e4m3(
         _ptr(q8), _ptr(k8), _ptr(scale), _ptr(qkv), _ptr(out), fmt, qkv.shape[0], qkv.shape[1], n_heads, head_dim,
         _stream(stream)))
+
+
+# ---------------------------------------------------------------- training pass of the attention sublayer
+
+_FMT_DTYPES = {FMT_BF16: (torch.bfloat16, torch.int16, torch.uint16), FMT_F16: (torch.float16, torch.int16, torch.uint16),
+               FMT_F32: (torch.float32,)}
+
+
+def _on_device(**tensors) -> None:
+    """Every tensor is in the current device's memory (the library runs on the current device)."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _of(name: str, t: Optional[torch.Tensor], shape, dtypes) -> None:
+    if t is None:
+        return
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _rows(name: str, t: torch.Tensor, batch: int, seq: int, cols: int, fmt: int):
+    """(pointer, leading dimension) of a [batch, seq, cols] view with unit column stride whose batch
+    elements lie seq rows apart."""
+    if fmt not in (FMT_BF16, FMT_F16):
+        raise ValueError(f"fmt {fmt} is not a 16-bit format")
+    _of(name, t, (batch, seq, cols), _FMT_DTYPES[fmt])
+    if seq > 1:
+        ld = t.stride(1)
+    else:
+        ld = t.stride(0) if batch > 1 else -(-cols // 8) * 8
+    if t.stride(2) != 1 or (batch > 1 and t.stride(0) != seq * ld):
+        raise ValueError(f"{name} has strides {t.stride()}: columns must be adjacent and elements seq rows apart")
+    return t.data_ptr(), ld
+
+
+def _ws(workspace: Optional[torch.Tensor]):
+    if workspace is None:
+        return None, 0
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def qknorm_mrope_out(qkv: torch.Tensor, qk: torch.Tensor, cfg: BlockConfig, n_text: int, grid_h: int, grid_w: int,
+                     g_q: torch.Tensor, g_k: torch.Tensor, t_img: int = -1, pos: Optional[torch.Tensor] = None,
+                     text_lens: Optional[torch.Tensor] = None, key_lens: Optional[torch.Tensor] = None,
+                     fmt: int = FMT_BF16, stream=None) -> None:
+    """QK-RMSNorm + M-RoPE of the raw q, k in ``qkv`` [B, S, 3d] into ``qk`` [B, S, 2d]; ``key_lens`` (int32 [B])
+    receives each element's token count."""
+    B, S, d = qkv.shape[0], n_text + grid_h * grid_w, cfg.d_model
+    _of("qkv", qkv, (B, S, 3 * d), _FMT_DTYPES[fmt])
+    _of("qk", qk, (B, S, 2 * d), _FMT_DTYPES[fmt])
+    _qk_args(cfg, B, S, g_q, g_k, pos, text_lens)
+    _of("key_lens", key_lens, (B,), (torch.int32,))
+    _on_device(qkv=qkv, qk=qk, g_q=g_q, g_k=g_k, pos=pos, text_lens=text_lens, key_lens=key_lens)
+    _check("dit_qknorm_mrope_out", lib().dit_qknorm_mrope_out(
+        _ptr(qkv), _ptr(qk), fmt, B, n_text, grid_h, grid_w, t_img, _ptr(pos), _ptr(text_lens), _ptr(key_lens),
+        ctypes.byref(cfg), _ptr(g_q), _ptr(g_k), _stream(stream)))
+
+
+def _qk_args(cfg, B, S, g_q, g_k, pos, text_lens) -> None:
+    _of("g_q", g_q, (cfg.head_dim,), _FMT_DTYPES[FMT_BF16])
+    _of("g_k", g_k, (cfg.head_dim,), _FMT_DTYPES[FMT_BF16])
+    _of("pos", pos, (S, 3), (torch.int32,))
+    _of("text_lens", text_lens, (B,), (torch.int32,))
+
+
+def qknorm_mrope_backward_workspace_bytes(cfg: BlockConfig, batch: int, seq: int) -> int:
+    return int(lib().dit_qknorm_mrope_backward_workspace_bytes(ctypes.byref(cfg), batch, seq))
+
+
+def qknorm_mrope_backward(qkv: torch.Tensor, dqk: torch.Tensor, dx: torch.Tensor, cfg: BlockConfig, n_text: int,
+                          grid_h: int, grid_w: int, g_q: torch.Tensor, g_k: torch.Tensor, dg_q: torch.Tensor,
+                          dg_k: torch.Tensor, workspace: torch.Tensor, t_img: int = -1,
+                          pos: Optional[torch.Tensor] = None, text_lens: Optional[torch.Tensor] = None,
+                          fmt: int = FMT_BF16, stream=None) -> None:
+    """Gradients of the raw q, k (``dx``) and of the gains (fp32 [hd]) from those of the rotated ones (``dqk``);
+    both [B, S, 2d] views, e.g. the first 2d columns of a [B, S, 3d] buffer, and possibly the same one."""
+    B, S, d = qkv.shape[0], n_text + grid_h * grid_w, cfg.d_model
+    _of("qkv", qkv, (B, S, 3 * d), _FMT_DTYPES[fmt])
+    _qk_args(cfg, B, S, g_q, g_k, pos, text_lens)
+    _of("dg_q", dg_q, (cfg.head_dim,), (torch.float32,))
+    _of("dg_k", dg_k, (cfg.head_dim,), (torch.float32,))
+    p_in, ld_in = _rows("dqk", dqk, B, S, 2 * d, fmt)
+    p_out, ld_out = _rows("dx", dx, B, S, 2 * d, fmt)
+    _on_device(qkv=qkv, dqk=dqk, dx=dx, g_q=g_q, g_k=g_k, dg_q=dg_q, dg_k=dg_k, pos=pos, text_lens=text_lens,
+               workspace=workspace)
+    _check("dit_qknorm_mrope_backward", lib().dit_qknorm_mrope_backward(
+        _ptr(qkv), p_in, ld_in, p_out, ld_out, _ptr(dg_q), _ptr(dg_k), fmt, B, n_text, grid_h, grid_w, t_img,
+        _ptr(pos), _ptr(text_lens), ctypes.byref(cfg), _ptr(g_q), _ptr(g_k), *_ws(workspace), _stream(stream)))
+
+
+def joint_attention_lse_workspace_bytes(batch: int, seq: int, n_heads: int, head_dim: int) -> int:
+    return int(lib().dit_joint_attention_lse_workspace_bytes(batch, seq, n_heads, head_dim))
+
+
+def joint_attention_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
+                        n_heads: int, head_dim: int, workspace: Optional[torch.Tensor] = None,
+                        key_lens: Optional[torch.Tensor] = None, fmt: int = FMT_BF16, stream=None) -> None:
+    """Joint attention of [B, S, d] views q, k, v into ``out`` [B, S, d] and ``lse`` fp32 [B, H, S]; with
+    ``key_lens`` (int32 [B]) only each element's leading rows take part and a workspace is needed."""
+    B, S, d = q.shape[0], q.shape[1], n_heads * head_dim
+    views = [a for n, t in (("q", q), ("k", k), ("v", v)) for a in _rows(n, t, B, S, d, fmt)]
+    _of("out", out, (B, S, d), _FMT_DTYPES[fmt])
+    _of("lse", lse, (B, n_heads, S), (torch.float32,))
+    _of("key_lens", key_lens, (B,), (torch.int32,))
+    _on_device(q=q, k=k, v=v, out=out, lse=lse, key_lens=key_lens, workspace=workspace)
+    _check("dit_joint_attention_lse", lib().dit_joint_attention_lse(
+        *views, _ptr(out), _ptr(lse), fmt, B, S, n_heads, head_dim, _ptr(key_lens), *_ws(workspace), _stream(stream)))
+
+
+def joint_attention_backward_workspace_bytes(batch: int, seq: int, n_heads: int, head_dim: int) -> int:
+    return int(lib().dit_joint_attention_backward_workspace_bytes(batch, seq, n_heads, head_dim))
+
+
+def joint_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, dout: torch.Tensor,
+                             lse: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor, n_heads: int,
+                             head_dim: int, workspace: torch.Tensor, key_lens: Optional[torch.Tensor] = None,
+                             fmt: int = FMT_BF16, stream=None) -> None:
+    """Gradients dq, dk, dv ([B, S, d] views) of ``joint_attention_lse`` from ``dout`` [B, S, d]."""
+    B, S, d = q.shape[0], q.shape[1], n_heads * head_dim
+    ins = [a for n, t in (("q", q), ("k", k), ("v", v)) for a in _rows(n, t, B, S, d, fmt)]
+    grads = [a for n, t in (("dq", dq), ("dk", dk), ("dv", dv)) for a in _rows(n, t, B, S, d, fmt)]
+    _of("out", out, (B, S, d), _FMT_DTYPES[fmt])
+    _of("dout", dout, (B, S, d), _FMT_DTYPES[fmt])
+    _of("lse", lse, (B, n_heads, S), (torch.float32,))
+    _of("key_lens", key_lens, (B,), (torch.int32,))
+    _on_device(q=q, k=k, v=v, out=out, dout=dout, lse=lse, dq=dq, dk=dk, dv=dv, key_lens=key_lens,
+               workspace=workspace)
+    _check("dit_joint_attention_backward", lib().dit_joint_attention_backward(
+        *ins, _ptr(out), _ptr(dout), _ptr(lse), *grads, fmt, B, S, n_heads, head_dim, _ptr(key_lens),
+        *_ws(workspace), _stream(stream)))
+
+
+def rmsnorm_rows_backward_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().dit_rmsnorm_rows_backward_workspace_bytes(rows, cols))
+
+
+def rmsnorm_rows_backward(x: torch.Tensor, g: torch.Tensor, dy: torch.Tensor, dx: torch.Tensor, dg: torch.Tensor,
+                          eps: float, workspace: torch.Tensor, dres: Optional[torch.Tensor] = None,
+                          x_fmt: int = FMT_BF16, dy_fmt: int = FMT_BF16, dx_fmt: int = FMT_BF16, stream=None) -> None:
+    """dx (+ ``dres``, the gradient past the norm) and dg (fp32 [cols]) of ``rmsnorm_rows``."""
+    cols = x.shape[-1]
+    _of("x", x, x.shape, _FMT_DTYPES[x_fmt])
+    _of("g", g, (cols,), _FMT_DTYPES[FMT_BF16])
+    _of("dy", dy, x.shape, _FMT_DTYPES[dy_fmt])
+    _of("dres", dres, x.shape, _FMT_DTYPES[dx_fmt])
+    _of("dx", dx, x.shape, _FMT_DTYPES[dx_fmt])
+    _of("dg", dg, (cols,), (torch.float32,))
+    _on_device(x=x, g=g, dy=dy, dx=dx, dg=dg, dres=dres, workspace=workspace)
+    _check("dit_rmsnorm_rows_backward", lib().dit_rmsnorm_rows_backward(
+        _ptr(x), x_fmt, _ptr(g), _ptr(dy), dy_fmt, _ptr(dres), _ptr(dx), dx_fmt, _ptr(dg), x.numel() // cols, cols,
+        eps, *_ws(workspace), _stream(stream)))
 
 
 KERNEL_TAGS = {1: "rope_table", 2: "rmsnorm", 3: "gemm_qkv", 4: "qknorm_mrope", 5: "attention", 6: "gemm_o",

@@ -39,8 +39,15 @@
 // of hd bytes per row), S = Q K^T is issued as kind::f8f6f4 pair MMAs (K = 32 per instruction)
 // and the two static scales of q and k multiply the softmax's log2(e)/sqrt(hd) factor; V, P and
 // P V are as above.
+// Form for the gradient (LSE): q, k and v are separate views, the log-sum-exp of every row is
+// written beside the output, and in a padded batch the rows at or beyond an element's count take
+// no part on either side: zeros in the output and the log-sum-exps, query tiles made of nothing
+// else cut to one key block.  What the masked rows hold does not matter, infinities and NaN
+// included: a masked logit is replaced, and the value block in which the tokens end comes from a
+// zero-padded copy (tm_vt), since P = 0 times a NaN value would be NaN inside the tensor core.
 #include "common.cuh"
 #include "qk8.h"
+#include "train.h"
 
 namespace jab {
 namespace attn {
@@ -119,11 +126,13 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 }
 
 // Q8: tm_q / tm_k map the e4m3 q8 / k8 buffers ([B, S, d] bytes), qk_scale[0..1] their scales.
-template <int HD, int F, bool Q8>
+// LSE: tm_q / tm_k / tm_v map q, k and v on their own, tm_vt the zero-padded last value blocks.
+template <int HD, int F, bool Q8, bool LSE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, uint16_t* __restrict__ out, int batch, int seq,
-                     int n_heads, const int32_t* __restrict__ kv_len, const float* __restrict__ qk_scale,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_vt,
+                     uint16_t* __restrict__ out, float* __restrict__ lse, int batch, int seq, int n_heads,
+                     const int32_t* __restrict__ kv_len, const float* __restrict__ qk_scale,
                      const KernelGuard guard) {
   using L = Layout<HD, Q8>;
   constexpr bool kF16 = F == FMT_F16;
@@ -157,8 +166,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   const int ntile = (seq + 4 * BQ - 1) / (4 * BQ);
   const int items = batch * n_heads * ntile;
   const int d = n_heads * HD;
+  const int k_off = LSE ? 0 : d, v_off = LSE ? 0 : 2 * d;  // columns of k and v in their tensor maps
   struct Item {
     int b, head, q0, nkv, nb;  // q0: this CTA's first row of tile A (tile t starts at q0 + 2 BQ t)
+    int live;                  // LSE: rows of the element that take part
+    bool tail;                 // LSE: the last value block comes from tm_vt
   };
   auto item = [&](int i) {
     Item it;
@@ -168,6 +180,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     it.q0 = qt * 4 * BQ + static_cast<int>(rank) * BQ;
     // keys of this batch element: all of them, or its key count (clamped to [1, seq])
     it.nkv = kv_len == nullptr ? seq : min(max(kv_len[it.b], 1), seq);
+    if constexpr (LSE) {
+      it.live = kv_len == nullptr ? seq : min(max(kv_len[it.b], 0), seq);
+      const bool any = qt * 4 * BQ < it.live;
+      if (!any) it.nkv = 1;  // no row takes part: one block, its result replaced by zeros
+      it.tail = any && it.live < seq && it.live % BKV != 0;
+    }
     it.nb = (it.nkv + BKV - 1) / BKV;
     return it;
   };
@@ -254,11 +272,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                              it.b);
           } else {
             for (int c = 0; c < HD / 64; ++c)
-              tma_load_3d_pair(sK + st * L::K_BYTES + c * L::K_SLAB, &tm_k, kbar, d + it.head * HD + 64 * c,
+              tma_load_3d_pair(sK + st * L::K_BYTES + c * L::K_SLAB, &tm_k, kbar, k_off + it.head * HD + 64 * c,
                                j * BKV + 64 * static_cast<int>(rank), it.b);
           }
-          tma_load_3d_pair(sV + st * L::V_BYTES, &tm_v, vbar,
-                           2 * d + it.head * HD + static_cast<int>(rank) * (HD / 2), j * BKV, it.b);
+          const bool from_tail = LSE && it.tail && j == it.nb - 1;
+          tma_load_3d_pair(sV + st * L::V_BYTES, from_tail ? &tm_vt : &tm_v, vbar,
+                           v_off + it.head * HD + static_cast<int>(rank) * (HD / 2), from_tail ? 0 : j * BKV, it.b);
         }
         __syncwarp();
         ++issued;
@@ -516,6 +535,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const float inv_l = 1.f / l;
       const int row = it.q0 + 2 * BQ * t + r;
       uint16_t* dst = out + (static_cast<size_t>(it.b) * seq + row) * d + it.head * HD;
+      if constexpr (LSE) {
+        // m_used and l are in log2 units of the scaled logits
+        if (row < seq)
+          lse[(static_cast<size_t>(it.b) * n_heads + it.head) * seq + row] =
+              row < it.live ? (m_used + log2f(l)) * 0.6931471805599453f : 0.f;
+      }
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c) {
         uint32_t raw[32];
@@ -526,7 +551,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           for (int q = 0; q < 4; ++q) {
             float o[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = __uint_as_float(raw[8 * q + k]) * inv_l;
+            for (int k = 0; k < 8; ++k) {
+              o[k] = __uint_as_float(raw[8 * q + k]) * inv_l;
+              if (LSE && row >= it.live) o[k] = 0.f;
+            }
             store8<F>(dst + 32 * c, q, o);
           }
         }
@@ -548,13 +576,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   }
 }
 
-template <int HD, int F, bool Q8 = false>
+template <int HD, int F, bool Q8 = false, bool LSE = false>
 cudaError_t launch_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, void* out, int batch,
                       int seq, int n_heads, const int32_t* kv_len, const KernelGuard& g, cudaStream_t s,
-                      const float* qk_scale = nullptr) {
+                      const float* qk_scale = nullptr, const CUtensorMap* tvt = nullptr, float* lse = nullptr) {
   using L = Layout<HD, Q8>;
   cudaError_t e =
-      cudaFuncSetAttribute(attention_kernel<HD, F, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+      cudaFuncSetAttribute(attention_kernel<HD, F, Q8, LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
   if (e != cudaSuccess) return e;
   // persistent: one CTA pair per SM pair at most, each walking work items (b, head, 512 queries)
   const long long items = static_cast<long long>(batch) * n_heads * ((seq + 4 * BQ - 1) / (4 * BQ));
@@ -564,8 +592,9 @@ cudaError_t launch_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   const long long pairs = items < sms / 2 ? items : sms / 2;
   if (items >= (1ll << 31) || pairs < 1) return cudaErrorInvalidValue;
   dim3 grid(static_cast<unsigned>(2 * pairs), 1, 1);
-  return launch_pdl(attention_kernel<HD, F, Q8>, grid, dim3(THREADS), L::SMEM, s, tq, tk, tv,
-                    static_cast<uint16_t*>(out), batch, seq, n_heads, kv_len, qk_scale, g);
+  return launch_pdl(attention_kernel<HD, F, Q8, LSE>, grid, dim3(THREADS), L::SMEM, s, tq, tk, tv,
+                    tvt != nullptr ? *tvt : tv, static_cast<uint16_t*>(out), lse, batch, seq, n_heads, kv_len,
+                    qk_scale, g);
 }
 
 }  // namespace attn
@@ -626,4 +655,62 @@ cudaError_t launch_attention_q8(const uint8_t* q8, const uint8_t* k8, const floa
   return fmt == FMT_F16 ? attn::launch_hd<64, FMT_F16, true>(tq, tk, tv, out, batch, seq, n_heads, kv_len, g, s, scale)
                         : attn::launch_hd<64, FMT_BF16, true>(tq, tk, tv, out, batch, seq, n_heads, kv_len, g, s, scale);
 }
+
+// One CTA per (row of the block, element); the element's last block, zero-padded.
+__global__ void tail_rows_kernel(const uint16_t* __restrict__ src, int64_t ld, uint16_t* __restrict__ dst, int seq,
+                                 int cols, const int32_t* __restrict__ key_lens) {
+  pdl_wait_then_release();
+  const int r = blockIdx.x, b = blockIdx.y;
+  const int n = min(max(key_lens[b], 0), seq);
+  if (n == seq || n % attn::BKV == 0) return;
+  const int row = n / attn::BKV * attn::BKV + r;
+  const uint4* from = reinterpret_cast<const uint4*>(src + (static_cast<int64_t>(b) * seq + row) * ld);
+  uint4* to = reinterpret_cast<uint4*>(dst + (static_cast<int64_t>(b) * attn::BKV + r) * cols);
+  for (int i = threadIdx.x; i < cols / 8; i += blockDim.x) to[i] = row < n ? from[i] : make_uint4(0u, 0u, 0u, 0u);
+}
+
+cudaError_t launch_tail_rows(Rows src, void* dst, int batch, int seq, int cols, const int32_t* key_lens,
+                             cudaStream_t s) {
+  return launch_pdl(tail_rows_kernel, dim3(attn::BKV, static_cast<unsigned>(batch)), dim3(256), 0, s,
+                    static_cast<const uint16_t*>(src.p), src.ld, static_cast<uint16_t*>(dst), seq, cols, key_lens);
+}
+
+size_t attention_lse_workspace(int batch, int seq, int n_heads, int head_dim) {
+  (void)seq;
+  return static_cast<size_t>(batch) * attn::BKV * n_heads * head_dim * 2;
+}
+
+cudaError_t launch_attention_lse(Rows q, Rows k, Rows v, void* out, float* lse, int fmt, int batch, int seq,
+                                 int n_heads, int head_dim, const int32_t* key_lens, void* workspace,
+                                 const KernelGuard& g, cudaStream_t s) {
+  const int d = n_heads * head_dim;
+  const CUtensorMapDataType dt = fmt == FMT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  auto map = [&](CUtensorMap* m, Rows r, int rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swz) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(rows), static_cast<uint64_t>(batch)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(r.ld) * 2, static_cast<uint64_t>(rows) * r.ld * 2};
+    const uint32_t box[3] = {box_cols, box_rows, 1};
+    return make_tmap(m, dt, 3, const_cast<void*>(r.p), dims, strides, box, swz);
+  };
+  const CUtensorMapSwizzle swz_v = head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  const uint32_t half = static_cast<uint32_t>(head_dim / 2);
+  CUtensorMap tq, tk, tv, tvt;
+  if (!map(&tq, q, seq, 64, attn::BQ, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !map(&tk, k, seq, 64, attn::BKV / 2, CU_TENSOR_MAP_SWIZZLE_128B) || !map(&tv, v, seq, half, attn::BKV, swz_v))
+    return cudaErrorInvalidValue;
+  tvt = tv;
+  if (key_lens != nullptr) {
+    if (!map(&tvt, Rows{workspace, d}, attn::BKV, half, attn::BKV, swz_v)) return cudaErrorInvalidValue;
+    const cudaError_t e = launch_tail_rows(v, workspace, batch, seq, d, key_lens, s);
+    if (e != cudaSuccess) return e;
+  }
+  auto run = [&](auto fn) { return fn(tq, tk, tv, out, batch, seq, n_heads, key_lens, g, s, nullptr, &tvt, lse); };
+  if (head_dim == 128)
+    return fmt == FMT_F16 ? run(attn::launch_hd<128, FMT_F16, false, true>)
+                          : run(attn::launch_hd<128, FMT_BF16, false, true>);
+  if (head_dim == 64)
+    return fmt == FMT_F16 ? run(attn::launch_hd<64, FMT_F16, false, true>)
+                          : run(attn::launch_hd<64, FMT_BF16, false, true>);
+  return cudaErrorInvalidValue;
+}
+
 }  // namespace jab

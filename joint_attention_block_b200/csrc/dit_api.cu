@@ -10,6 +10,7 @@
 #include "jab_dit.h"
 #include "internal.h"
 #include "qk8.h"
+#include "train.h"
 
 namespace jab {
 
@@ -721,6 +722,158 @@ int dit_tokens_from_latent(const float* z, const void* text, void* x, int batch,
   if (!aligned16(z) || !aligned16(text) || !aligned16(x)) return DIT_ERR_INVALID_ARG;
   return from_cuda(launch_denoise_pack(z, static_cast<const uint16_t*>(text), nullptr, static_cast<uint16_t*>(x),
                                        nullptr, batch, n_img, d_model, n_text, 0, as_stream(stream)));
+}
+
+// ---- the training pass through the attention sublayer
+
+namespace {
+
+// One CTA per (block of 128 rows, head, element) at most, heads and elements as grid dimensions.
+bool attn_shape_ok(int batch, int seq, int n_heads, int head_dim) {
+  if (batch <= 0 || seq <= 0 || n_heads <= 0 || batch > 65535 || n_heads > 65535) return false;
+  const int64_t tokens = static_cast<int64_t>(batch) * seq;
+  const int64_t blocks = (static_cast<int64_t>(seq) + 127) / 128 * n_heads * batch;
+  return tokens < (1ll << 31) / 16 && blocks < (1ll << 31) && static_cast<int64_t>(n_heads) * head_dim < (1ll << 24);
+}
+
+bool rows_ok(const void* p, int64_t ld, int64_t cols) {
+  return p != nullptr && aligned16(p) && ld >= cols && ld % 8 == 0 && ld < (1ll << 31);
+}
+
+bool ws_ok(const void* p, size_t bytes, size_t need) {
+  return p != nullptr && bytes >= need && (reinterpret_cast<uintptr_t>(p) & 255u) == 0;
+}
+
+}  // namespace
+
+int dit_qknorm_mrope_out(const void* qkv, void* qk, int fmt, int batch, int n_text, int grid_h, int grid_w, int t_img,
+                         const int32_t* pos, const int32_t* text_lens, int32_t* key_lens, const dit_block_config* cfg,
+                         const void* g_q, const void* g_k, void* stream) {
+  clear_stale_error();
+  const int st = check_config(cfg);
+  if (st != DIT_OK) return st;
+  if (!shape_ok(batch, n_text, grid_h, grid_w) || qkv == nullptr || qk == nullptr || g_q == nullptr || g_k == nullptr)
+    return DIT_ERR_INVALID_ARG;
+  if (fmt != FMT_BF16 && fmt != FMT_F16) return DIT_ERR_INVALID_ARG;
+  if (qkv == qk || (pos != nullptr && text_lens != nullptr)) return DIT_ERR_INVALID_ARG;
+  if (!aligned16(qkv) || !aligned16(qk) || !aligned16(g_q) || !aligned16(g_k)) return DIT_ERR_INVALID_ARG;
+  cudaStream_t s = as_stream(stream);
+  prof_mark(s, DIT_KERNEL_QKNORM_MROPE);
+  const cudaError_t e = launch_qknorm_mrope_out(
+      qkv, qk, fmt, batch, n_text + grid_h * grid_w, cfg->n_heads, cfg->head_dim, n_text, grid_w, grid_h * grid_w,
+      t_img, pos, text_lens, key_lens, cfg->rope_sections, cfg->rope_theta, static_cast<const uint16_t*>(g_q),
+      static_cast<const uint16_t*>(g_k), cfg->eps, s);
+  prof_mark(s, DIT_KERNEL_END);
+  return from_cuda(e);
+}
+
+size_t dit_qknorm_mrope_backward_workspace_bytes(const dit_block_config* cfg, int batch, int seq) {
+  if (check_config(cfg) != DIT_OK || batch <= 0 || seq <= 0) return 0;
+  return align256(qknorm_mrope_bwd_workspace(static_cast<int64_t>(batch) * seq, cfg->head_dim));
+}
+
+int dit_qknorm_mrope_backward(const void* qkv, const void* dqk, int64_t ld_dqk, void* dx, int64_t ld_dx, float* dg_q,
+                              float* dg_k, int fmt, int batch, int n_text, int grid_h, int grid_w, int t_img,
+                              const int32_t* pos, const int32_t* text_lens, const dit_block_config* cfg,
+                              const void* g_q, const void* g_k, void* workspace, size_t ws_bytes, void* stream) {
+  clear_stale_error();
+  const int st = check_config(cfg);
+  if (st != DIT_OK) return st;
+  if (!shape_ok(batch, n_text, grid_h, grid_w) || qkv == nullptr || g_q == nullptr || g_k == nullptr ||
+      dg_q == nullptr || dg_k == nullptr || dg_q == dg_k)
+    return DIT_ERR_INVALID_ARG;
+  if (fmt != FMT_BF16 && fmt != FMT_F16) return DIT_ERR_INVALID_ARG;
+  const int64_t cols = 2ll * cfg->d_model;
+  if (!rows_ok(dqk, ld_dqk, cols) || !rows_ok(dx, ld_dx, cols) || dx == qkv || (dx == dqk && ld_dx != ld_dqk) ||
+      (pos != nullptr && text_lens != nullptr))
+    return DIT_ERR_INVALID_ARG;
+  if (!aligned16(qkv) || !aligned16(g_q) || !aligned16(g_k)) return DIT_ERR_INVALID_ARG;
+  const int S = n_text + grid_h * grid_w;
+  if (!ws_ok(workspace, ws_bytes, dit_qknorm_mrope_backward_workspace_bytes(cfg, batch, S))) return DIT_ERR_WORKSPACE;
+  return from_cuda(launch_qknorm_mrope_bwd(qkv, Rows{dqk, ld_dqk}, Rows{dx, ld_dx}, dg_q, dg_k, fmt, batch, S,
+                                           cfg->n_heads, cfg->head_dim, n_text, grid_w, grid_h * grid_w, t_img, pos,
+                                           text_lens, cfg->rope_sections, cfg->rope_theta,
+                                           static_cast<const uint16_t*>(g_q), static_cast<const uint16_t*>(g_k),
+                                           cfg->eps, workspace, as_stream(stream)));
+}
+
+size_t dit_joint_attention_lse_workspace_bytes(int batch, int seq, int n_heads, int head_dim) {
+  if ((head_dim != 64 && head_dim != 128) || !attn_shape_ok(batch, seq, n_heads, head_dim)) return 0;
+  return align256(attention_lse_workspace(batch, seq, n_heads, head_dim));
+}
+
+int dit_joint_attention_lse(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                            void* out, float* lse, int fmt, int batch, int seq, int n_heads, int head_dim,
+                            const int32_t* key_lens, void* workspace, size_t ws_bytes, void* stream) {
+  clear_stale_error();
+  if (head_dim != 64 && head_dim != 128) return DIT_ERR_UNSUPPORTED;
+  if (!attn_shape_ok(batch, seq, n_heads, head_dim) || (fmt != FMT_BF16 && fmt != FMT_F16)) return DIT_ERR_INVALID_ARG;
+  const int64_t d = static_cast<int64_t>(n_heads) * head_dim;
+  if (!rows_ok(q, ld_q, d) || !rows_ok(k, ld_k, d) || !rows_ok(v, ld_v, d) || !rows_ok(out, d, d) || lse == nullptr)
+    return DIT_ERR_INVALID_ARG;
+  if (out == q || out == k || out == v) return DIT_ERR_INVALID_ARG;
+  if (key_lens != nullptr &&
+      !ws_ok(workspace, ws_bytes, dit_joint_attention_lse_workspace_bytes(batch, seq, n_heads, head_dim)))
+    return DIT_ERR_WORKSPACE;
+  KernelGuard g;
+  if (current_guard(&g) != cudaSuccess) return DIT_ERR_CUDA;
+  return from_cuda(launch_attention_lse(Rows{q, ld_q}, Rows{k, ld_k}, Rows{v, ld_v}, out, lse, fmt, batch, seq,
+                                        n_heads, head_dim, key_lens, workspace, g, as_stream(stream)));
+}
+
+size_t dit_joint_attention_backward_workspace_bytes(int batch, int seq, int n_heads, int head_dim) {
+  if ((head_dim != 64 && head_dim != 128) || !attn_shape_ok(batch, seq, n_heads, head_dim)) return 0;
+  return align256(attention_bwd_workspace(batch, seq, n_heads, head_dim));
+}
+
+int dit_joint_attention_backward(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v, int64_t ld_v,
+                                 const void* out, const void* dout, const float* lse, void* dq, int64_t ld_dq,
+                                 void* dk, int64_t ld_dk, void* dv, int64_t ld_dv, int fmt, int batch, int seq,
+                                 int n_heads, int head_dim, const int32_t* key_lens, void* workspace, size_t ws_bytes,
+                                 void* stream) {
+  clear_stale_error();
+  if (head_dim != 64 && head_dim != 128) return DIT_ERR_UNSUPPORTED;
+  if (!attn_shape_ok(batch, seq, n_heads, head_dim) || (fmt != FMT_BF16 && fmt != FMT_F16)) return DIT_ERR_INVALID_ARG;
+  const int64_t d = static_cast<int64_t>(n_heads) * head_dim;
+  if (!rows_ok(q, ld_q, d) || !rows_ok(k, ld_k, d) || !rows_ok(v, ld_v, d) || !rows_ok(out, d, d) ||
+      !rows_ok(dout, d, d) || !rows_ok(dq, ld_dq, d) || !rows_ok(dk, ld_dk, d) || !rows_ok(dv, ld_dv, d) ||
+      lse == nullptr)
+    return DIT_ERR_INVALID_ARG;
+  const void* ins[5] = {q, k, v, out, dout};
+  for (const void* p : ins)
+    if (p == dq || p == dk || p == dv) return DIT_ERR_INVALID_ARG;
+  if (dq == dk || dq == dv || dk == dv) return DIT_ERR_INVALID_ARG;
+  if (!ws_ok(workspace, ws_bytes, dit_joint_attention_backward_workspace_bytes(batch, seq, n_heads, head_dim)))
+    return DIT_ERR_WORKSPACE;
+  KernelGuard g;
+  if (current_guard(&g) != cudaSuccess) return DIT_ERR_CUDA;
+  return from_cuda(launch_attention_bwd(Rows{q, ld_q}, Rows{k, ld_k}, Rows{v, ld_v}, out, dout, lse, Rows{dq, ld_dq},
+                                        Rows{dk, ld_dk}, Rows{dv, ld_dv}, fmt, batch, seq, n_heads, head_dim,
+                                        key_lens, workspace, g, as_stream(stream)));
+}
+
+size_t dit_rmsnorm_rows_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols <= 0 || cols % 8 != 0 || cols > 8192) return 0;
+  const size_t n = rmsnorm_bwd_workspace(rows, cols);
+  return align256(n > 0 ? n : 1);
+}
+
+int dit_rmsnorm_rows_backward(const void* x, int x_fmt, const void* g, const void* dy, int dy_fmt, const void* dres,
+                              void* dx, int dx_fmt, float* dg, int64_t rows, int64_t cols, float eps, void* workspace,
+                              size_t ws_bytes, void* stream) {
+  clear_stale_error();
+  if (rows < 0 || cols <= 0 || cols % 8 != 0 || rows > (1ll << 31) - 1) return DIT_ERR_INVALID_ARG;
+  if (cols > 8192) return DIT_ERR_UNSUPPORTED;  // a row stays in registers
+  if ((x_fmt != FMT_BF16 && x_fmt != FMT_F32) || dy_fmt < FMT_BF16 || dy_fmt > FMT_F32 || dx_fmt < FMT_BF16 ||
+      dx_fmt > FMT_F32)
+    return DIT_ERR_INVALID_ARG;
+  if (dg == nullptr || !aligned16(dg)) return DIT_ERR_INVALID_ARG;
+  if (rows == 0) return from_cuda(cudaMemsetAsync(dg, 0, static_cast<size_t>(cols) * 4, as_stream(stream)));
+  if (x == nullptr || g == nullptr || dy == nullptr || dx == nullptr || dx == x || dx == dy) return DIT_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(g) || !aligned16(dy) || !aligned16(dres) || !aligned16(dx)) return DIT_ERR_INVALID_ARG;
+  if (!ws_ok(workspace, ws_bytes, dit_rmsnorm_rows_backward_workspace_bytes(rows, cols))) return DIT_ERR_WORKSPACE;
+  return from_cuda(launch_rmsnorm_bwd(x, x_fmt, static_cast<const uint16_t*>(g), dy, dy_fmt, dres, dx, dx_fmt, dg,
+                                      rows, cols, eps, workspace, as_stream(stream)));
 }
 
 }  // extern "C"

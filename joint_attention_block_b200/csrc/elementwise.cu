@@ -6,6 +6,8 @@
 
 #include "common.cuh"
 #include "qk8.h"
+#include "rope.cuh"
+#include "train.h"
 
 namespace jab {
 
@@ -427,33 +429,6 @@ cudaError_t launch_denoise_update(float* z, const uint16_t* out_c, const uint16_
 
 // ------------------------------------------------------------------ positions and angle tables
 
-// Text token j -> (j, j, j); image cell (r, c) in raster order -> (t_img, r, c).
-// Positions and inverse frequencies of the rotary embedding, passed by value to the QK-norm kernel.
-struct RopeArgs {
-  int n_text, grid_w, n_img, t_img;  // t_img < 0: n_text (or L_b in a padded batch)
-  const int32_t* pos;                // [S, 3] or NULL (ignored when text_lens is given)
-  const int32_t* text_lens;          // [batch] or NULL
-  int32_t* kv_len;                   // [batch], written when text_lens is given
-  int sec_t, sec_h;                  // rotary pairs on the t and h axes (w takes the rest)
-  float inv_freq[64];                // fp32(theta^(-2i/hd)), i < hd/2
-};
-
-__device__ __forceinline__ void token_position(int s, int n_text, int grid_w, int t_img, const int32_t* pos, int& pt,
-                                               int& ph, int& pw) {
-  if (pos != nullptr) {
-    pt = pos[3 * s];
-    ph = pos[3 * s + 1];
-    pw = pos[3 * s + 2];
-  } else if (s < n_text) {
-    pt = ph = pw = s;
-  } else {
-    const int i = s - n_text;
-    pt = t_img;
-    ph = i / grid_w;
-    pw = i - ph * grid_w;
-  }
-}
-
 __global__ void positions_kernel(int n_text, int grid_h, int grid_w, int t_img, int32_t* pos) {
   const int S = n_text + grid_h * grid_w;
   const int s = blockIdx.x * blockDim.x + threadIdx.x;
@@ -491,11 +466,13 @@ cudaError_t launch_positions(int n_text, int grid_h, int grid_w, int t_img, int3
 // ([B * S, d] bytes), each divided by one static scale, fp32(fp32(sqrt(hd)) * max|g|) / 448 (the
 // norm of a normalised head vector is at most sqrt(hd) * max|g| and the rotations keep it, so no
 // code saturates), which the CTA of token 0 also stores in o8.scale[0] (q) and [1] (k).
-template <int F, bool Q8>
+// OUT (for the gradient, which needs the raw q and k): the results go to qk_out [B * S, 2d]
+// instead (q columns, then k columns).
+template <int F, bool Q8, bool OUT = false>
 __global__ void __launch_bounds__(512, 2)  // <= 64 registers: four 256-thread CTAs per SM
     qknorm_mrope_kernel(uint16_t* __restrict__ qkv, int seq, int n_heads, int head_dim, RopeArgs ra,
                                     const uint16_t* __restrict__ g_q, const uint16_t* __restrict__ g_k, float eps,
-                                    QK8Out o8) {
+                                    QK8Out o8, uint16_t* __restrict__ qk_out) {
   __shared__ float s_cos[64], s_sin[64];
   __shared__ float s_gmax[2];  // Q8: max |g_q|, max |g_k|
   pdl_wait_then_release();
@@ -520,33 +497,10 @@ __global__ void __launch_bounds__(512, 2)  // <= 64 registers: four 256-thread C
   const uint4 rkb = *reinterpret_cast<const uint4*>(vk + half + 8 * c);
   {
     int pt = 0, ph = 0, pw = 0;
-    if (ra.text_lens != nullptr) {
-      const int L = min(max(ra.text_lens[b], 0), ra.n_text);
-      if (s == 0 && threadIdx.x == 0) ra.kv_len[b] = L + ra.n_img;
-      if (s < L) {
-        pt = ph = pw = s;
-      } else if (s < L + ra.n_img) {
-        const int k = s - L;
-        pt = ra.t_img < 0 ? L : ra.t_img;
-        ph = k / ra.grid_w;
-        pw = k - ph * ra.grid_w;
-      }
-    } else {
-      token_position(s, ra.n_text, ra.grid_w, ra.t_img < 0 ? ra.n_text : ra.t_img, ra.pos, pt, ph, pw);
-    }
-    for (int i = threadIdx.x; i < half; i += blockDim.x) {
-      const int p = i < ra.sec_t ? pt : (i < ra.sec_t + ra.sec_h ? ph : pw);
-      // the angle p * inv_freq_i is exact in fp64; it is reduced by the nearest multiple of 2 pi
-      // in fp64 (error ~1e-13 for the angles of any image), rounded once to fp32 in [-pi, pi],
-      // and its sine and cosine taken in fp32
-      const double x = static_cast<double>(p) * static_cast<double>(ra.inv_freq[i]);
-      const double k = rint(x * 0.15915494309189535);
-      const float r = static_cast<float>(fma(-k, 6.283185307179586, x));
-      float sn, cs;
-      sincosf(r, &sn, &cs);
-      s_cos[i] = cs;
-      s_sin[i] = sn;
-    }
+    const int count = rope_position(ra, b, s, pt, ph, pw);
+    if (ra.kv_len != nullptr && s == 0 && threadIdx.x == 0) ra.kv_len[b] = count;
+    for (int i = threadIdx.x; i < half; i += blockDim.x)
+      rope_angle(ra, i, i < ra.sec_t ? pt : (i < ra.sec_t + ra.sec_h ? ph : pw), s_cos[i], s_sin[i]);
   }
   if constexpr (Q8) {
     if (threadIdx.x < 32) {  // max |g| of both gains, hd <= 128 values each: four per lane
@@ -616,8 +570,9 @@ __global__ void __launch_bounds__(512, 2)  // <= 64 registers: four 256-thread C
   };
   if constexpr (!Q8) {
     if (live) {
-      rotate(rqa, rqb, rq, g_q, vq);
-      rotate(rka, rkb, rk, g_k, vk);
+      uint16_t* dst = OUT ? qk_out + bs * (2 * static_cast<int64_t>(d)) + h * head_dim : vq;
+      rotate(rqa, rqb, rq, g_q, dst);
+      rotate(rka, rkb, rk, g_k, dst + d);
     }
   } else {
     const float root = __fsqrt_rn(static_cast<float>(head_dim));
@@ -671,25 +626,15 @@ namespace {
 cudaError_t qknorm_mrope_impl(void* qkv, int fmt, int batch, int seq, int n_heads, int head_dim, int n_text,
                               int grid_w, int n_img, int t_img, const int32_t* pos, const int32_t* text_lens,
                               int32_t* kv_len, const int32_t sections[3], float theta, const uint16_t* g_q,
-                              const uint16_t* g_k, float eps, cudaStream_t s, const QK8Out* o8) {
+                              const uint16_t* g_k, float eps, cudaStream_t s, const QK8Out* o8,
+                              uint16_t* qk_out = nullptr) {
   const int64_t tokens = static_cast<int64_t>(batch) * seq;
   if (tokens <= 0 || n_heads <= 0) return cudaSuccess;
   if (head_dim != 64 && head_dim != 128) return cudaErrorInvalidValue;
-  if ((text_lens != nullptr) != (kv_len != nullptr)) return cudaErrorInvalidValue;
+  if (qk_out == nullptr && (text_lens != nullptr) != (kv_len != nullptr)) return cudaErrorInvalidValue;
   const int per_token = n_heads * (head_dim / 16);
   if (per_token > 512) return cudaErrorInvalidValue;  // the kernel's launch bound
-  RopeArgs ra;
-  ra.n_text = n_text;
-  ra.grid_w = grid_w > 0 ? grid_w : 1;
-  ra.n_img = n_img;
-  ra.t_img = t_img;
-  ra.pos = pos;
-  ra.text_lens = text_lens;
-  ra.kv_len = kv_len;
-  ra.sec_t = sections[0];
-  ra.sec_h = sections[1];
-  for (int i = 0; i < head_dim / 2; ++i)
-    ra.inv_freq[i] = static_cast<float>(std::pow(static_cast<double>(theta), -2.0 * i / head_dim));
+  const RopeArgs ra = rope_args(n_text, grid_w, n_img, t_img, pos, text_lens, kv_len, sections, theta, head_dim);
   const unsigned threads = static_cast<unsigned>((per_token + 31) / 32 * 32);
   const unsigned blocks = static_cast<unsigned>(tokens);
   uint16_t* q = static_cast<uint16_t*>(qkv);
@@ -699,21 +644,32 @@ cudaError_t qknorm_mrope_impl(void* qkv, int fmt, int batch, int seq, int n_head
       return cudaErrorInvalidValue;
     if (fmt == FMT_F16)
       launch_pdl(qknorm_mrope_kernel<FMT_F16, true>, dim3(blocks), dim3(threads), 0, s, q, seq, n_heads, head_dim, ra,
-                 g_q, g_k, eps, *o8);
+                 g_q, g_k, eps, *o8, nullptr);
     else if (fmt == FMT_BF16)
       launch_pdl(qknorm_mrope_kernel<FMT_BF16, true>, dim3(blocks), dim3(threads), 0, s, q, seq, n_heads, head_dim, ra,
-                 g_q, g_k, eps, *o8);
+                 g_q, g_k, eps, *o8, nullptr);
     else
       return cudaErrorInvalidValue;
     return cudaGetLastError();
   }
   const QK8Out none{nullptr, nullptr, nullptr};
+  if (qk_out != nullptr) {
+    if (fmt == FMT_F16)
+      launch_pdl(qknorm_mrope_kernel<FMT_F16, false, true>, dim3(blocks), dim3(threads), 0, s, q, seq, n_heads,
+                 head_dim, ra, g_q, g_k, eps, none, qk_out);
+    else if (fmt == FMT_BF16)
+      launch_pdl(qknorm_mrope_kernel<FMT_BF16, false, true>, dim3(blocks), dim3(threads), 0, s, q, seq, n_heads,
+                 head_dim, ra, g_q, g_k, eps, none, qk_out);
+    else
+      return cudaErrorInvalidValue;
+    return cudaGetLastError();
+  }
   if (fmt == FMT_F16)
     launch_pdl(qknorm_mrope_kernel<FMT_F16, false>, dim3(blocks), dim3(threads), 0, s, q, seq, n_heads, head_dim, ra,
-               g_q, g_k, eps, none);
+               g_q, g_k, eps, none, nullptr);
   else if (fmt == FMT_BF16)
     launch_pdl(qknorm_mrope_kernel<FMT_BF16, false>, dim3(blocks), dim3(threads), 0, s, q, seq, n_heads, head_dim, ra,
-               g_q, g_k, eps, none);
+               g_q, g_k, eps, none, nullptr);
   else
     return cudaErrorInvalidValue;
   return cudaGetLastError();
@@ -736,6 +692,15 @@ cudaError_t launch_qknorm_mrope_e4m3(const void* qkv, int fmt, int batch, int se
                                      cudaStream_t s) {
   return qknorm_mrope_impl(const_cast<void*>(qkv), fmt, batch, seq, n_heads, head_dim, n_text, grid_w, n_img, t_img,
                            pos, text_lens, kv_len, sections, theta, g_q, g_k, eps, s, &o8);
+}
+
+cudaError_t launch_qknorm_mrope_out(const void* qkv, void* qk, int fmt, int batch, int seq, int n_heads, int head_dim,
+                                    int n_text, int grid_w, int n_img, int t_img, const int32_t* pos,
+                                    const int32_t* text_lens, int32_t* key_lens, const int32_t sections[3],
+                                    float theta, const uint16_t* g_q, const uint16_t* g_k, float eps, cudaStream_t s) {
+  return qknorm_mrope_impl(const_cast<void*>(qkv), fmt, batch, seq, n_heads, head_dim, n_text, grid_w, n_img, t_img,
+                           pos, text_lens, key_lens, sections, theta, g_q, g_k, eps, s, nullptr,
+                           static_cast<uint16_t*>(qk));
 }
 
 // ------------------------------------------------------------------ bounded-wait self test
