@@ -46,6 +46,7 @@
 // included: a masked logit is replaced, and the value block in which the tokens end comes from a
 // zero-padded copy (tm_vt), since P = 0 times a NaN value would be NaN inside the tensor core.
 #include "common.cuh"
+#include "pipeline.cuh"
 #include "qk8.h"
 #include "train.h"
 
@@ -226,6 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // ---------------- TMA producer: per work item this CTA's rows of Q_A and Q_B (once the
     // previous item's S MMAs have read Q), then its K and V halves of every key block, through
     // the key/value ring that runs on across items
+    const bool one = elect_one();
     int issued = 0;    // key blocks issued, all items
     int q_issued = 0;  // work items whose Q load was issued
     int ui = 0;        // work items started
@@ -237,7 +239,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         ok = false;
         break;
       }
-      if (lane == 0) {
+      if (one) {
         if (leader) mbar_arrive_expect_tx(q_full, 2 * 2 * L::Q_TILE);
         const uint32_t qbar = mapa_shared(smem_u32(q_full), 0);
         for (int t = 0; t < 2; ++t) {
@@ -260,7 +262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           ok = false;
           break;
         }
-        if (lane == 0) {
+        if (one) {
           if (leader) {
             mbar_arrive_expect_tx(&k_full[st], 2 * L::K_BYTES);
             mbar_arrive_expect_tx(&v_full[st], 2 * L::V_BYTES);
@@ -300,6 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else if (warp == 1) {
     // ---------------- MMA issuer (leader only)
     if (leader) {
+      const bool one = elect_one();
       // kind::f16 for 16-bit q, k; kind::f8f6f4 (type code 0: e4m3) for Q8
       constexpr uint32_t idesc_s = idesc_f16kind(2 * BQ, BKV, Q8 ? true : kF16, false, false);
       constexpr uint32_t idesc_o = idesc_f16kind(2 * BQ, HD, kF16, false, true);
@@ -349,7 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                        where_code(ERR_TIMEOUT_ATTN_MMA, rank, gb));
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
+        if (one) {
           issue_s(0, gb);
           issue_s(1, gb);
           if (nb == 1) mma_commit_pair(q_empty, 0x3);  // the item's last S MMAs are issued: Q free after them
@@ -372,7 +375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                           where_code(ERR_TIMEOUT_ATTN_MMA, 5, g)));
           if (!ok) break;
           tc_fence_after();
-          if (lane == 0) {
+          if (one) {
             issue_pv(0, g, j);
             if (next) issue_s(0, g + 1);  // overwrites P_A only after P V_A has read it (in-order issue)
           }
@@ -383,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                           where_code(ERR_TIMEOUT_ATTN_MMA, 6, g)));
           if (!ok) break;
           tc_fence_after();
-          if (lane == 0) {
+          if (one) {
             issue_pv(1, g, j);
             mma_commit_pair(&kv_empty[st], 0x3);  // K_g and V_g fully consumed by both tiles
             if (next) {
@@ -393,11 +396,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           __syncwarp();
         }
-        if (ok && lane == 0) mma_commit_pair(o_full, 0x3);  // this item's O final
+        if (ok && one) mma_commit_pair(o_full, 0x3);  // this item's O final
         __syncwarp();
         gb += nb;
       }
-      if (lane == 0) mma_commit_pair(drain_bar, 0x3);  // all MMAs retired before either CTA frees TMEM
+      if (one) mma_commit_pair(drain_bar, 0x3);  // all MMAs retired before either CTA frees TMEM
       __syncwarp();
     }
     mbar_wait(drain_bar, 0u, guard, abort_flag, where_code(ERR_TIMEOUT_ATTN_DRAIN, rank, 1), true);
