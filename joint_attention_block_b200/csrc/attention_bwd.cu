@@ -5,8 +5,8 @@
 // Three launches:
 //   bwd_prep_kernel  delta and the row log-sum-exps in log2 units, padded to whole blocks of 128
 //                    rows, and what the other two need to know of the data (see below)
-//   bwd_dq_kernel    256 queries per CTA pair, over all key blocks
 //   bwd_dkv_kernel   256 keys per CTA pair, over all query blocks
+//   bwd_dq_kernel    256 queries per CTA pair, over all key blocks
 // S and dP are computed in both of the latter, seven products instead of five: dQ is summed over
 // the keys and dK, dV over the queries, and a single pass would have to add one of them up in
 // global memory, by fp32 atomics (whose order changes the result from run to run) or through
@@ -30,21 +30,29 @@
 namespace jab {
 namespace abwd {
 
-constexpr int T = 128;   // rows of an own tile per CTA; keys of a block in dq
-constexpr int BQ = 96;   // queries of a block in dkv
-constexpr int COLS = 32;  // columns of a block per elementwise thread: a warp for each 32 x 32 piece
+constexpr int T = 128;  // rows of an own tile per CTA
 constexpr int TMEM_COLS = 512;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float P_SHIFT = 15.f;  // f16: P is held as 2^15 P
 
+// The shape of one pass: blocks of R rows of the streamed axis, COLS of them per elementwise thread (a
+// warp works on a 32 x COLS piece), SLOTS blocks of operands in flight.
+struct DkvShape {
+  static constexpr int R = 80, COLS = 16, SLOTS = 3, CUTS_B = 2;
+};
+struct DqShape {
+  static constexpr int R = 128, COLS = 32, SLOTS = 3, CUTS_B = 1;
+};
+
 __host__ __device__ inline int blocks_of(int seq) { return (seq + T - 1) / T; }
 
-// Per (b, h), nblk = the blocks of 128 rows and one more (blocks of 96 rows end inside it):
-// ws.lse2 / ws.delta [B, H, nblk * 128]; norms2 [B, H, nblk]: the block's max |dO_q|^2 and
-// max |V_k|^2 (f16 only); tails: zero-padded copies [3: q, k, dO][B, 128, H hd].
+// Per (b, h), nblk = the blocks of 128 rows and one more (blocks of any R <= 128 rows end inside it):
+// nlse2 / ndelta [B, H, nblk * 128], -log2(e) lse and -delta; norms2 [B, H, nblk]: the block's max
+// |dO_q|^2 and max |V_k|^2 (f16 only); tails: zero-padded copies [3: q, k, dO][B, 128, H hd] of the
+// block in which the tokens end.
 struct Workspace {
-  float* lse2;
-  float* delta;
+  float* nlse2;
+  float* ndelta;
   float2* norms2;
   uint16_t* tails;
   size_t bytes;
@@ -58,8 +66,8 @@ static Workspace carve(void* base, int batch, int seq, int n_heads, int head_dim
   const size_t vec = align256(bh * nblk * T * 4), nrm = align256(bh * nblk * 8);
   const size_t tail = align256(static_cast<size_t>(batch) * T * n_heads * head_dim * 2 * 3);
   uint8_t* b = static_cast<uint8_t*>(base);
-  w.lse2 = reinterpret_cast<float*>(b);
-  w.delta = reinterpret_cast<float*>(b + vec);
+  w.nlse2 = reinterpret_cast<float*>(b);
+  w.ndelta = reinterpret_cast<float*>(b + vec);
   w.norms2 = reinterpret_cast<float2*>(b + 2 * vec);
   w.tails = reinterpret_cast<uint16_t*>(b + 2 * vec + nrm);
   w.bytes = 2 * vec + nrm + tail;
@@ -77,7 +85,7 @@ struct PrepArgs {
   int64_t ldq, ldk, ldv;
   const float* lse;
   const int32_t* key_lens;
-  float *lse2, *delta;
+  float *nlse2, *ndelta;
   float2* norms2;
   uint16_t* tails;
   int batch, seq, n_heads;
@@ -98,8 +106,8 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepArgs a) {
   const int d = a.n_heads * HD;
   const int c = static_cast<int>(threadIdx.x) % LANES, r0 = static_cast<int>(threadIdx.x) / LANES;
   const int64_t bh = static_cast<int64_t>(b) * a.n_heads + h;
-  float* lse2 = a.lse2 + (bh * nblk + blk) * T;
-  float* delta = a.delta + (bh * nblk + blk) * T;
+  float* nlse2 = a.nlse2 + (bh * nblk + blk) * T;
+  float* ndelta = a.ndelta + (bh * nblk + blk) * T;
   float mdo = 0.f, mv = 0.f;
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
@@ -135,8 +143,8 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepArgs a) {
     mv = fmaxf(mv, sv);
     if (c == 0) {
       // rows that take no part: exp2(s - inf) = 0
-      delta[r] = dot;
-      lse2[r] = row < n ? a.lse[bh * a.seq + row] * LOG2E - (F == FMT_F16 ? P_SHIFT : 0.f) : INFINITY;
+      ndelta[r] = -dot;
+      nlse2[r] = row < n ? (F == FMT_F16 ? P_SHIFT : 0.f) - a.lse[bh * a.seq + row] * LOG2E : -INFINITY;
     }
   }
   if constexpr (F == FMT_F16) {
@@ -155,22 +163,22 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepArgs a) {
       a.norms2[bh * nblk + blk] = make_float2(mdo, mv);
     }
   }
-  // k: the block of 128 rows in which the tokens end; q and dO: the block of 96
-  const bool tk = has_tail(n, a.seq, T) && blk == n / T;
-  const int q0 = n / BQ * BQ;
-  const bool tq = has_tail(n, a.seq, BQ) && blk * T < q0 + BQ && blk * T + T > q0;
+  // k: the block in which the tokens end in dq's blocks; q and dO: in dkv's
+  constexpr int RK = DqShape::R, RQ = DkvShape::R;
+  const int k0 = n / RK * RK, q0 = n / RQ * RQ;
+  auto reaches = [&](int row0, int rows) { return blk * T < row0 + rows && blk * T + T > row0; };
+  const bool tk = has_tail(n, a.seq, RK) && reaches(k0, RK), tq = has_tail(n, a.seq, RQ) && reaches(q0, RQ);
   if (tk || tq) {
     const size_t one = static_cast<size_t>(a.batch) * T * d;
     for (int p = 0; p < PASSES; ++p) {
-      const int r = p * ROWS + r0;
-      const int row = blk * T + r;
+      const int row = blk * T + p * ROWS + r0;
       const int64_t at = static_cast<int64_t>(b) * a.seq + row;
       auto put = [&](const uint16_t* src, int64_t ld, int which, int dst_row) {
         const uint4 x = row < n ? reinterpret_cast<const uint4*>(src + at * ld + h * HD)[c] : make_uint4(0u, 0u, 0u, 0u);
         reinterpret_cast<uint4*>(a.tails + which * one + (static_cast<size_t>(b) * T + dst_row) * d + h * HD)[c] = x;
       };
-      if (tk) put(a.k, a.ldk, 1, r);
-      if (tq && row >= q0 && row < q0 + BQ) {
+      if (tk && row >= k0 && row < k0 + RK) put(a.k, a.ldk, 1, row - k0);
+      if (tq && row >= q0 && row < q0 + RQ) {
         put(a.q, a.ldq, 0, row - q0);
         put(a.dout, d, 2, row - q0);
       }
@@ -199,30 +207,35 @@ __device__ __forceinline__ float ds_shift(const float2* norms2, int nblk) {
   return l > -100.f && l < 100.f ? floorf(14.f - l) : 0.f;
 }
 
-// Shared memory of one CTA.  Own tiles: 128 rows x HD (K and V in dkv, Q and dO in dq), slabs of 64
-// columns, 128-byte swizzle.  Ring slots hold this CTA's half of a block of R rows of the other axis,
-// in one of two cuts of the same size: "rows", R / 2 rows x HD, the B operand of a product over HD, or
-// "cols", R rows x HD / 2, the B operand of a product over the rows.
-template <int HD, int R, int RINGS>
+// Shared memory and threads of one CTA.  Own tiles A, B: 128 rows x HD (K and V in dkv, Q and dO in
+// dq), slabs of 64 columns, 128-byte swizzle.  Two rings hold this CTA's halves of the streamed blocks,
+// in two cuts of the same size: ring A "rows", R / 2 rows x HD, the B operands of the products over HD
+// (S, dP); ring B "cols", R rows x HD / 2, those of the products over the rows.
+template <int HD, class Shape>
 struct Layout {
-  static constexpr int N = 3;  // slots of a ring
+  static constexpr int R = Shape::R, COLS = Shape::COLS, N = Shape::SLOTS;
   static constexpr int PARTS = R / COLS;
   static constexpr int EW_WARPS = 4 * PARTS;
-  static constexpr int THREADS = 64 + 32 * EW_WARPS;
+  static constexpr int FIRST_EW = 3;  // after the loading and the two issuing warps
+  static constexpr int THREADS = 32 * (FIRST_EW + EW_WARPS);
+  static constexpr int NV = 5;  // slots of the row vectors (dkv)
   static constexpr int SLAB = T * 128;
   static constexpr int TILE = (HD / 64) * SLAB;
   static constexpr int RSLAB = R / 2 * 128;
-  static constexpr int CUT = R * HD;  // bytes of one ring slot, either cut
+  static constexpr int CUT = R * HD;
+  static constexpr int SLOT_A = 2 * CUT, SLOT_B = Shape::CUTS_B * CUT;
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = OFF_A + TILE;
-  static constexpr int OFF_RING = OFF_B + TILE;
-  static constexpr int OFF_VEC = OFF_RING + RINGS * N * CUT;  // dkv: [N][lse2 | delta], R each
-  static constexpr int OFF_BAR = OFF_VEC + N * 2 * R * 4;
-  static constexpr int NUM_BARS = 48;
+  static constexpr int OFF_RING_A = OFF_B + TILE;
+  static constexpr int OFF_RING_B = OFF_RING_A + N * SLOT_A;
+  static constexpr int OFF_VEC = OFF_RING_B + N * SLOT_B;  // dkv: [NV][nlse2 | ndelta], R each
+  static constexpr int OFF_BAR = OFF_VEC + NV * 2 * R * 4;
+  static constexpr int NUM_BARS = 4 * N + 4 + NV + 11;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static_assert(SMEM <= 232448, "227 KB of shared memory per CTA");
   static_assert(RSLAB % 1024 == 0 && CUT % 1024 == 0, "swizzled tiles keep their alignment");
+  static_assert(R % 16 == 0 && R % COLS == 0 && OFF_VEC % 16 == 0 && (R * 4) % 16 == 0, "");
 };
 
 // Global -> shared copy of a multiple of 16 bytes, both addresses 16-byte aligned.
@@ -243,7 +256,7 @@ template <class L, int HD>
 __device__ __forceinline__ void load_rows_cut(uint8_t* dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z,
                                               int rank) {
   for (int c = 0; c < HD / 64; ++c)
-    tma_load_3d_pair(dst + c * L::RSLAB, m, bar, x + 64 * c, y + L::RSLAB / 128 * rank, z);
+    tma_load_3d_pair(dst + c * L::RSLAB, m, bar, x + 64 * c, y + L::R / 2 * rank, z);
 }
 template <int HD>
 __device__ __forceinline__ void load_cols_cut(uint8_t* dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z,
@@ -252,8 +265,7 @@ __device__ __forceinline__ void load_cols_cut(uint8_t* dst, const CUtensorMap* m
 }
 
 // The descriptor of the same layout `bytes` further on.  One 32-bit add: the start address (in 16-byte
-// units) fills the low 14 bits and stays below 2^14 inside 227 KB.  Building each descriptor from its
-// address instead made the issuing lane the slowest part of the kernel (about 110 clocks per MMA).
+// units) fills the low 14 bits and stays below 2^14 inside 227 KB.
 __device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) {
   return (d & 0xFFFFFFFF00000000ull) | (static_cast<uint32_t>(d) + (bytes >> 4));
 }
@@ -261,63 +273,66 @@ __device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) {
 // D[256 x R] = A B^T over HD: A both CTAs' own tiles, B a block in the rows cut.
 template <class L, int HD, int F>
 __device__ __forceinline__ void mma_rows(uint32_t d, const uint8_t* a, const uint8_t* b) {
-  constexpr uint32_t idesc = idesc_f16kind(2 * T, L::RSLAB / 64, F == FMT_F16, false, false);
+  constexpr uint32_t idesc = idesc_f16kind(2 * T, L::R, F == FMT_F16, false, false);
   const uint64_t ad = smem_desc_sw128(smem_u32(a), 16, 1024), bd = smem_desc_sw128(smem_u32(b), 16, 1024);
 #pragma unroll
-  for (int kk = 0; kk < HD / 16; ++kk) {
-    constexpr int RS = L::RSLAB, AS = L::SLAB;
-    mma_f16kind_ss_pair(d, desc_at(ad, (kk >> 2) * AS + (kk & 3) * 32), desc_at(bd, (kk >> 2) * RS + (kk & 3) * 32),
-                        idesc, kk > 0 ? 1u : 0u);
-  }
+  for (int kk = 0; kk < HD / 16; ++kk)
+    mma_f16kind_ss_pair(d, desc_at(ad, (kk >> 2) * L::SLAB + (kk & 3) * 32),
+                        desc_at(bd, (kk >> 2) * L::RSLAB + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
 }
 
-// D[256 x HD] (+)= A[256 x R] B: A as 16-bit pairs in TMEM, 16 columns for every COLS = 32 values and
-// those pieces `step` columns apart; B a block in the cols cut, its rows being the contraction axis.
-template <int R, int HD, int F>
-__device__ __forceinline__ void mma_cols(uint32_t d, uint32_t a, int step, const uint8_t* b, bool accumulate) {
+// D[256 x HD] (+)= A[256 x R] B: A as 16-bit pairs in R / 2 TMEM columns, B a block in the cols cut, its
+// rows being the contraction axis.
+template <class L, int HD, int F>
+__device__ __forceinline__ void mma_cols(uint32_t d, uint32_t a, const uint8_t* b, bool accumulate) {
   constexpr uint32_t idesc = idesc_f16kind(2 * T, HD, F == FMT_F16, false, true);
   const uint64_t bd = HD == 128 ? smem_desc_sw128(smem_u32(b), 16, 8 * HD) : smem_desc_sw64(smem_u32(b), 16, 8 * HD);
 #pragma unroll
-  for (int kk = 0; kk < R / 16; ++kk)  // 16 rows of HD / 2 values
-    mma_f16kind_ts_pair(d, a + step * (kk >> 1) + 8 * (kk & 1), desc_at(bd, kk * 16 * HD), idesc,
-                        (accumulate || kk > 0) ? 1u : 0u);
+  for (int kk = 0; kk < L::R / 16; ++kk)  // 16 rows of HD / 2 values
+    mma_f16kind_ts_pair(d, a + 8 * kk, desc_at(bd, kk * 16 * HD), idesc, (accumulate || kk > 0) ? 1u : 0u);
 }
 
-__device__ __forceinline__ void get_part(uint32_t taddr, float (&v)[COLS]) {
-  static_assert(COLS == 32, "one TMEM load");
-  uint32_t a[32];
-  tmem_ld32(taddr, a);
-  tmem_ld_wait_regs(a);
-#pragma unroll
-  for (int k = 0; k < COLS; ++k) v[k] = __uint_as_float(a[k]);
+// COLS fp32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void get_cols(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void get_cols(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
-
-// A thread's values as 16-bit pairs into COLS / 2 columns.
-template <int F>
-__device__ __forceinline__ void put_part(uint32_t taddr, const float (&v)[COLS]) {
-  uint32_t pk[COLS / 2];
-#pragma unroll
-  for (int k = 0; k < COLS / 2; ++k) pk[k] = pack2<F>(v[2 * k], v[2 * k + 1]);
-  tmem_st16(taddr, pk);
-  tmem_st_wait();
+// Wait for this thread's TMEM loads; no use of r can move above it.
+__device__ __forceinline__ void got_cols(uint32_t (&r)[32]) { tmem_ld_wait_regs(r); }
+__device__ __forceinline__ void got_cols(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+               "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+// COLS / 2 columns of 16-bit pairs.
+__device__ __forceinline__ void put_cols(uint32_t taddr, const uint32_t (&r)[16]) { tmem_st16(taddr, r); }
+__device__ __forceinline__ void put_cols(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ float2 as_f2(const uint32_t* r) {
+  return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 // NC columns of one accumulator row (fp32 at taddr) times f into a 16-bit row, or zeros.
 template <int NC, int F>
 __device__ __forceinline__ void store_row(uint32_t taddr, float f, uint16_t* dst, bool in_range, bool live) {
+  uint32_t raw[NC];
+  get_cols(taddr, raw);
+  got_cols(raw);
+  if (in_range) {
 #pragma unroll
-  for (int c = 0; c < NC / 32; ++c) {
-    uint32_t raw[32];
-    tmem_ld32(taddr + 32 * c, raw);
-    tmem_ld_wait_regs(raw);
-    if (in_range) {
+    for (int q = 0; q < NC / 8; ++q) {
+      float o[8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float o[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[k] = live ? __uint_as_float(raw[8 * q + k]) * f : 0.f;
-        store8<F>(dst + 32 * c, q, o);
-      }
+      for (int k = 0; k < 8; ++k) o[k] = live ? __uint_as_float(raw[8 * q + k]) * f : 0.f;
+      store8<F>(dst, q, o);
     }
   }
 }
@@ -376,76 +391,185 @@ struct Item {
   int b, head, tt, n, nb;  // n: tokens of the element; nb: blocks of the other axis (0: no row takes part)
   int64_t bh;
 };
-__device__ __forceinline__ Item item_of(int i, int ntile, int n_heads, int seq, const int32_t* key_lens, int rows) {
+template <int R>
+__device__ __forceinline__ Item item_of(int i, int ntile, int n_heads, int seq, const int32_t* key_lens) {
   Item it;
   it.tt = i % ntile;
   it.bh = i / ntile;
   it.head = static_cast<int>(it.bh % n_heads);
   it.b = static_cast<int>(it.bh / n_heads);
   it.n = tokens_of(key_lens, it.b, seq);
-  it.nb = it.tt * 2 * T < it.n ? (it.n + rows - 1) / rows : 0;
+  it.nb = it.tt * 2 * T < it.n ? (it.n + R - 1) / R : 0;
   return it;
+}
+
+// What both passes share: two CTAs on two SMs (a cluster) own 256 rows of one head, 128 each, and walk
+// the other axis in blocks; the pair MMA (cta_group::2, M = 256) lets each CTA hold half of every block.
+// The kernels are persistent (pair p takes items p, p + pairs, ...; rings and barrier phases run on
+// across items) and every buffer between two steps has a barrier for each direction, so that a step
+// waits for its own operands only and nothing relies on the order of issue:
+//   warp 0            loads: the item's own tiles, per block ring A, ring B (and dkv's row vectors)
+//   warp 1, leader    S(u) once S(u-1) has been read into registers, dP(u) likewise
+//   warp 2, leader    the products with P and dS, once those are written (warp 2 holds the TMEM)
+//   the others        the elementwise step; thread = own row and COLS columns of the block
+// One lane of each issuing warp per pair runs the tensor cores of both SMs; with one warp for all
+// products its waits and commits took 1500 clocks a block, as long as the products.
+template <class L, int HD>
+struct Pipe {
+  uint8_t *tile_a, *tile_b, *mem_a, *mem_b;
+  float* vec;
+  Ring<1> at, bt;
+  Ring<L::N> ra, rb;
+  uint64_t *vec_full, *s_full, *s_empty, *dp_full, *dp_empty, *p_full, *p_empty, *ds_full, *ds_empty, *acc_full, *acc_empty,
+      *drain_bar;
+  uint32_t* tmem_slot;
+  volatile uint32_t* abort_flag;
+
+  __device__ __forceinline__ Pipe(uint8_t* smem, uint64_t* bars)
+      : tile_a(smem + L::OFF_A),
+        tile_b(smem + L::OFF_B),
+        mem_a(smem + L::OFF_RING_A),
+        mem_b(smem + L::OFF_RING_B),
+        vec(reinterpret_cast<float*>(smem + L::OFF_VEC)),
+        at(bars),
+        bt(bars + 2),
+        ra(bars + 4),
+        rb(bars + 4 + 2 * L::N) {
+    vec_full = bars + 4 + 4 * L::N;  // [NV] this CTA's copies
+    s_full = vec_full + L::NV;
+    s_empty = s_full + 1;      // leader; by every elementwise warp of both CTAs, as the ones marked *
+    dp_full = s_empty + 1;
+    dp_empty = dp_full + 1;    // *
+    p_full = dp_empty + 1;     // *
+    p_empty = p_full + 1;
+    ds_full = p_empty + 1;     // *
+    ds_empty = ds_full + 1;
+    acc_full = ds_empty + 1;
+    acc_empty = acc_full + 1;  // *
+    drain_bar = acc_empty + 1;
+    tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+    abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::OFF_MISC + 4);
+  }
+  __device__ __forceinline__ void init() const {
+    at.init();
+    bt.init();
+    ra.init();
+    rb.init();
+    for (int i = 0; i < L::NV; ++i) mbar_init(&vec_full[i], 1);
+    for (uint64_t* b : {s_full, dp_full, p_empty, ds_empty, acc_full}) mbar_init(b, 1);
+    for (uint64_t* b : {s_empty, dp_empty, p_full, ds_full, acc_empty}) mbar_init(b, 2 * L::EW_WARPS);
+    mbar_init(drain_bar, 2);  // both issuing warps
+    *abort_flag = 0u;
+    fence_barrier_init();
+  }
+};
+
+// Set-up and the end of both kernels.  Returns the TMEM base.
+template <class P>
+__device__ __forceinline__ uint32_t begin(const P& pipe) {
+  if (threadIdx.x == 0) pipe.init();
+  if (warp_id() == 2) tmem_alloc_pair(pipe.tmem_slot, TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before any remote arrive or TMA
+  tc_fence_after();
+  return *pipe.tmem_slot;
+}
+__device__ __forceinline__ void finish(uint32_t tmem) {
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the pair MMAs or remote arrives may touch it
+  if (warp_id() == 2) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, TMEM_COLS);
+  }
+}
+
+// Warp 1 of the leader: S and dP of every block.
+template <class L, int HD, int F>
+__device__ __forceinline__ void issue_s_dp(const Pipe<L, HD>& p, uint32_t t_s, uint32_t t_dp, int pair, int pairs,
+                                           int items, int ntile, int n_heads, int seq, const int32_t* key_lens,
+                                           const KernelGuard& guard) {
+  const bool one = elect_one();
+  auto where = [&](int k, int i) { return where_code(ERR_TIMEOUT_ABWD_MMA, k, i); };
+  bool ok = true;
+  int u = 0, ui = 0;
+  for (int i = pair; i < items && ok; i += pairs) {
+    const int nb = item_of<L::R>(i, ntile, n_heads, seq, key_lens).nb;
+    if (nb == 0) continue;
+    ok = p.at.wait_full(ui, guard, p.abort_flag, where(0, u));
+    for (int j = 0; j < nb && ok; ++j, ++u) {
+      const uint32_t prev = static_cast<uint32_t>(u - 1) & 1u;
+      const uint8_t* slot = p.mem_a + (u % L::N) * L::SLOT_A;
+      ok = p.ra.wait_full(u, guard, p.abort_flag, where(1, u)) &&
+           (u == 0 || mbar_wait(p.s_empty, prev, guard, p.abort_flag, where(2, u)));
+      if (!ok) break;
+      tc_fence_after();
+      if (one) {
+        mma_rows<L, HD, F>(t_s, p.tile_a, slot);
+        mma_commit_pair(p.s_full, 0x3);
+        if (j + 1 == nb) mma_commit_pair(&p.at.empty[0], 0x3);
+      }
+      __syncwarp();
+      ok = (j > 0 || p.bt.wait_full(ui, guard, p.abort_flag, where(3, u))) &&
+           (u == 0 || mbar_wait(p.dp_empty, prev, guard, p.abort_flag, where(4, u)));
+      if (!ok) break;
+      tc_fence_after();
+      if (one) {
+        mma_rows<L, HD, F>(t_dp, p.tile_b, slot + L::CUT);
+        mma_commit_pair(p.dp_full, 0x3);
+        mma_commit_pair(&p.ra.empty[u % L::N], 0x3);
+        if (j + 1 == nb) mma_commit_pair(&p.bt.empty[0], 0x3);
+      }
+      __syncwarp();
+    }
+    ++ui;
+  }
+  if (one) mma_commit_pair(p.drain_bar, 0x3);
+  __syncwarp();
+}
+
+// Copies a CTA may still have in flight when it leaves: the leader's barriers count both CTAs', and the
+// peer is held by the final cluster barrier until the leader has drained.
+template <class L, int HD>
+__device__ __forceinline__ void drain_loads(const Pipe<L, HD>& p, int n_at, int n_bt, int n_a, int n_b, int n_vec,
+                                            int rank, const KernelGuard& guard) {
+  const uint32_t wd = where_code(ERR_TIMEOUT_ABWD_DRAIN, rank, 0);
+  for (int v = n_vec > L::NV ? n_vec - L::NV : 0; v < n_vec; ++v)
+    mbar_wait(&p.vec_full[v % L::NV], static_cast<uint32_t>(v / L::NV) & 1u, guard, p.abort_flag, wd, true);
+  if (rank == 0) {
+    p.at.drain(n_at, guard, p.abort_flag, wd);
+    p.bt.drain(n_bt, guard, p.abort_flag, wd);
+    p.ra.drain(n_a, guard, p.abort_flag, wd);
+    p.rb.drain(n_b, guard, p.abort_flag, wd);
+  }
 }
 
 // ------------------------------------------------------------------ dK, dV
 
-// Two CTAs on two SMs (a cluster) share 256 keys of one head, 128 each, and walk the queries in blocks
-// of 96; the pair MMA (cta_group::2, M = 256) lets each CTA hold half of every query block.  The
-// products run with the keys as rows (S^T = K Q^T, dP^T = V dO^T), so that P^T and dS^T come out of the
-// elementwise step in the layout in which the tensor core reads an A operand from TMEM:
-// dV += P^T dO, dK += dS^T Q.
-// TMEM of each CTA: S^T 96 | dP^T 96 | P^T 48 | (16 unused) | dV | dK, 128 columns each; dS^T overwrites
-// dP^T as 16-bit pairs.  With blocks of 128 queries P^T has no columns of its own and must overwrite
-// S^T, so S(j+1) waits for dV(j), which waits for the whole exponential step of block j: 3420 clocks per
-// block of 128 against the products' 2048.  With 96, S(j+1) runs as soon as S(j) has been read into
-// registers and the elementwise warps never wait for it.
-// Persistent: pair p takes work items p, p + pairs, ...; rings and barrier phases run on across items.
-//   warp 0       loads.  Q and dO of a block come in both cuts, each with a ring of its own, since
-//                S frees Q's rows long before dK frees its columns
-//   warp 1       TMEM; in the leader one lane issues S(j+1) when S(j) has been read, dV(j) when P(j) is
-//                written, dK(j) and dP(j+1) when dS(j) is
-//   warps 2..13  P^T = exp2(c S^T - lse2), then dS^T = P^T (dP^T - delta); thread = key row and a third
-//                of the query columns; at the end of an item the rows of dV and dK.
+// Own rows: keys; streamed: queries.  The products run with the keys as rows (S^T = K Q^T,
+// dP^T = V dO^T), so that P^T and dS^T come out of the elementwise step in the layout in which the tensor
+// core reads an A operand from TMEM: dV += P^T dO, dK += dS^T Q.
+// Blocks of 80 queries: S^T 80, dP^T 80, P^T 40 and dS^T 40 columns beside dV and dK (128 each) are what
+// TMEM holds with a region of its own for each.  With 128 and P^T over S^T, dS^T over dP^T, S(j+1) waited for
+// dV(j) and dP(j+1) for dK(j): 3420 clocks a block against the products' 2048; with 96 and only
+// dS^T over dP^T 2030 against 1536.
 struct DkvMaps {
   CUtensorMap k, v, q_rows, q_cols, do_rows, do_cols, tq_rows, tq_cols, tdo_rows, tdo_cols;
 };
 template <int HD>
-using DkvLayout = Layout<HD, BQ, 4>;
+using DkvLayout = Layout<HD, DkvShape>;
 
 template <int HD, int F>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREADS, 1)
-    bwd_dkv_kernel(const __grid_constant__ DkvMaps tm, const float* __restrict__ lse2, const float* __restrict__ delta,
-                   const float2* __restrict__ norms2, OutRows dk, OutRows dv, int batch, int seq, int n_heads,
-                   const int32_t* __restrict__ key_lens, const KernelGuard guard) {
+    bwd_dkv_kernel(const __grid_constant__ DkvMaps tm, const float* __restrict__ nlse2,
+                   const float* __restrict__ ndelta, const float2* __restrict__ norms2, OutRows dk, OutRows dv,
+                   int batch, int seq, int n_heads, const int32_t* __restrict__ key_lens, const KernelGuard guard) {
   using L = DkvLayout<HD>;
-  constexpr int N = L::N;
+  constexpr int R = L::R, COLS = L::COLS, N = L::N, NV = L::NV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sK = smem + L::OFF_A;
-  uint8_t* sV = smem + L::OFF_B;
-  uint8_t* sQr = smem + L::OFF_RING;
-  uint8_t* sOr = sQr + N * L::CUT;
-  uint8_t* sOc = sOr + N * L::CUT;
-  uint8_t* sQc = sOc + N * L::CUT;
-  float* sVec = reinterpret_cast<float*>(smem + L::OFF_VEC);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-  const Ring<N> qr(bars), dor(bars + 2 * N), doc(bars + 4 * N), qc(bars + 6 * N);
-  const Ring<1> kt(bars + 8 * N), vt(bars + 8 * N + 2);
-  uint64_t* vec_full = bars + 8 * N + 4;  // [N] this CTA's copies
-  uint64_t* vec_empty = vec_full + N;     // [N] the elementwise warps of this CTA
-  uint64_t* s_full = vec_empty + N;
-  uint64_t* s_empty = s_full + 1;          // leader: every elementwise warp of both CTAs
-  uint64_t* dp_full = s_empty + 1;
-  uint64_t* p_full = dp_full + 1;          // leader: every elementwise warp of both CTAs
-  uint64_t* p_empty = p_full + 1;          // dV has read P
-  uint64_t* ds_full = p_empty + 1;         // leader: every elementwise warp of both CTAs
-  uint64_t* acc_full = ds_full + 1;
-  uint64_t* acc_empty = acc_full + 1;      // leader: every elementwise warp of both CTAs
-  uint64_t* drain_bar = acc_empty + 1;
-  static_assert(8 * N + 4 + 2 * N + 9 <= L::NUM_BARS, "barriers fit");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
-  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::OFF_MISC + 4);
-
+  const Pipe<L, HD> p(smem, reinterpret_cast<uint64_t*>(smem + L::OFF_BAR));
   const int warp = static_cast<int>(warp_id());
   const int lane = static_cast<int>(lane_id());
   const int rank = static_cast<int>(cluster_ctarank());
@@ -454,210 +578,133 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
   const int nblk = blocks_of(seq) + 1;
   const int ntile = (seq + 2 * T - 1) / (2 * T);
   const int items = batch * n_heads * ntile;
-
-  if (threadIdx.x == 0) {
-    qr.init();
-    dor.init();
-    doc.init();
-    qc.init();
-    kt.init();
-    vt.init();
-    for (int i = 0; i < N; ++i) {
-      mbar_init(&vec_full[i], 1);
-      mbar_init(&vec_empty[i], L::EW_WARPS);
-    }
-    mbar_init(s_full, 1);
-    mbar_init(s_empty, 2 * L::EW_WARPS);
-    mbar_init(dp_full, 1);
-    mbar_init(p_full, 2 * L::EW_WARPS);
-    mbar_init(p_empty, 1);
-    mbar_init(ds_full, 2 * L::EW_WARPS);
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 2 * L::EW_WARPS);
-    mbar_init(drain_bar, 1);
-    *abort_flag = 0u;
-    fence_barrier_init();
-  }
-  if (warp == 1) tmem_alloc_pair(tmem_slot, TMEM_COLS);
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();  // both CTAs' barriers exist before any remote arrive or TMA
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const uint32_t t_s = tmem, t_dp = tmem + 96, t_p = tmem + 192, t_dv = tmem + 256, t_dk = tmem + 384;
+  const uint32_t tmem = begin(p);
+  constexpr int C_DP = R, C_P = 2 * R, C_DS = C_P + R / 2, C_DV = 256, C_DK = 384;
+  static_assert(C_DS + R / 2 <= C_DV, "TMEM columns");
   pdl_wait_then_release();
 
   if (warp == 0) {
     const bool one = elect_one();
-    int u = 0, ui = 0;
-    int n_qr = 0, n_or = 0, n_oc = 0, n_qc = 0, n_k = 0, n_v = 0, n_vec = 0;
+    int u = 0, ui = 0, n_b = 0, n_bt = 0, n_at = 0;
     bool ok = true;
     auto where = [&](int i) { return where_code(ERR_TIMEOUT_ABWD_PRODUCER, rank, i); };
     for (int i = pair; i < items && ok; i += pairs) {
-      const Item it = item_of(i, ntile, n_heads, seq, key_lens, BQ);
+      const Item it = item_of<R>(i, ntile, n_heads, seq, key_lens);
       if (it.nb == 0) continue;
-      const bool tail = has_tail(it.n, seq, BQ);
+      const bool tail = has_tail(it.n, seq, R);
       const int x = it.head * HD, row0 = it.tt * 2 * T + rank * T;
-      ok = kt.wait_empty(ui, guard, abort_flag, where(0xFFFF));
+      ok = p.at.wait_empty(ui, guard, p.abort_flag, where(0xFFFF));
       if (!ok) break;
-      if (one) load_tile<L, HD>(sK, &tm.k, kt.arm(ui, leader, 2 * L::TILE), x, row0, it.b);
-      ++n_k;
+      if (one) load_tile<L, HD>(p.tile_a, &tm.k, p.at.arm(ui, leader, 2 * L::TILE), x, row0, it.b);
+      ++n_at;
       __syncwarp();
-      for (int j = 0; j < it.nb; ++j, ++u) {
+      for (int j = 0; j < it.nb && ok; ++j) {
         const bool tl = tail && j == it.nb - 1;
-        const int y = tl ? 0 : j * BQ, st = u % N;
-        ok = qr.wait_empty(u, guard, abort_flag, where(u));
-        if (!ok) break;
-        if (one)
-          load_rows_cut<L, HD>(sQr + st * L::CUT, tl ? &tm.tq_rows : &tm.q_rows, qr.arm(u, leader, 2 * L::CUT), x, y,
-                               it.b, rank);
-        ++n_qr;
-        __syncwarp();
-        ok = mbar_wait(&vec_empty[st], (static_cast<uint32_t>(u / N) & 1u) ^ 1u, guard, abort_flag, where(u));
+        const int y = tl ? 0 : j * R, sv = u % NV;
+        // the slot is free when dP(u - N) is done; that product waited until every warp was done with dP of
+        // the block before, so with all blocks up to u - 5, whose row vectors' slot is reused here
+        ok = p.ra.wait_empty(u, guard, p.abort_flag, where(u));
         if (!ok) break;
         if (one) {
-          float* vec = sVec + st * 2 * BQ;
-          mbar_arrive_expect_tx(&vec_full[st], 2 * BQ * 4);
-          bulk_load(vec, lse2 + it.bh * nblk * T + j * BQ, BQ * 4, &vec_full[st]);
-          bulk_load(vec + BQ, delta + it.bh * nblk * T + j * BQ, BQ * 4, &vec_full[st]);
+          uint8_t* slot = p.mem_a + (u % N) * L::SLOT_A;
+          const uint32_t bar = p.ra.arm(u, leader, 2 * L::SLOT_A);
+          load_rows_cut<L, HD>(slot, tl ? &tm.tq_rows : &tm.q_rows, bar, x, y, it.b, rank);
+          load_rows_cut<L, HD>(slot + L::CUT, tl ? &tm.tdo_rows : &tm.do_rows, bar, x, y, it.b, rank);
+          float* vec = p.vec + sv * 2 * R;
+          mbar_arrive_expect_tx(&p.vec_full[sv], 2 * R * 4);
+          bulk_load(vec, nlse2 + it.bh * nblk * T + j * R, R * 4, &p.vec_full[sv]);
+          bulk_load(vec + R, ndelta + it.bh * nblk * T + j * R, R * 4, &p.vec_full[sv]);
         }
-        ++n_vec;
         __syncwarp();
+        ++u;
         if (j == 0) {
-          ok = vt.wait_empty(ui, guard, abort_flag, where(0xFFFE));
+          ok = p.bt.wait_empty(ui, guard, p.abort_flag, where(0xFFFE));
           if (!ok) break;
-          if (one) load_tile<L, HD>(sV, &tm.v, vt.arm(ui, leader, 2 * L::TILE), x, row0, it.b);
-          ++n_v;
+          if (one) load_tile<L, HD>(p.tile_b, &tm.v, p.bt.arm(ui, leader, 2 * L::TILE), x, row0, it.b);
+          ++n_bt;
           __syncwarp();
         }
-        ok = dor.wait_empty(u, guard, abort_flag, where(u));
+        ok = p.rb.wait_empty(n_b, guard, p.abort_flag, where(n_b));
         if (!ok) break;
-        if (one)
-          load_rows_cut<L, HD>(sOr + st * L::CUT, tl ? &tm.tdo_rows : &tm.do_rows, dor.arm(u, leader, 2 * L::CUT), x, y,
-                               it.b, rank);
-        ++n_or;
-        __syncwarp();
-        ok = doc.wait_empty(u, guard, abort_flag, where(u));
-        if (!ok) break;
-        if (one)
-          load_cols_cut<HD>(sOc + st * L::CUT, tl ? &tm.tdo_cols : &tm.do_cols, doc.arm(u, leader, 2 * L::CUT), x, y,
-                            it.b, rank);
-        ++n_oc;
-        __syncwarp();
-        ok = qc.wait_empty(u, guard, abort_flag, where(u));
-        if (!ok) break;
-        if (one)
-          load_cols_cut<HD>(sQc + st * L::CUT, tl ? &tm.tq_cols : &tm.q_cols, qc.arm(u, leader, 2 * L::CUT), x, y, it.b,
-                            rank);
-        ++n_qc;
+        if (one) {
+          uint8_t* slot = p.mem_b + (n_b % N) * L::SLOT_B;
+          const uint32_t bar = p.rb.arm(n_b, leader, 2 * L::SLOT_B);
+          load_cols_cut<HD>(slot, tl ? &tm.tdo_cols : &tm.do_cols, bar, x, y, it.b, rank);
+          load_cols_cut<HD>(slot + L::CUT, tl ? &tm.tq_cols : &tm.q_cols, bar, x, y, it.b, rank);
+        }
+        ++n_b;
         __syncwarp();
       }
       ++ui;
     }
-    // Never leave with copies in flight: the leader's barriers count both CTAs' copies, and the peer is
-    // held by the final cluster barrier until the leader has drained.
-    const uint32_t wd = where_code(ERR_TIMEOUT_ABWD_DRAIN, rank, 0);
-    for (int v = n_vec > N ? n_vec - N : 0; v < n_vec; ++v)
-      mbar_wait(&vec_full[v % N], static_cast<uint32_t>(v / N) & 1u, guard, abort_flag, wd, true);
-    if (leader) {
-      kt.drain(n_k, guard, abort_flag, wd);
-      vt.drain(n_v, guard, abort_flag, wd);
-      qr.drain(n_qr, guard, abort_flag, wd);
-      dor.drain(n_or, guard, abort_flag, wd);
-      doc.drain(n_oc, guard, abort_flag, wd);
-      qc.drain(n_qc, guard, abort_flag, wd);
-    }
+    drain_loads(p, n_at, n_bt, u, n_b, u, rank, guard);
   } else if (warp == 1) {
-    const bool one = elect_one();
+    if (leader)
+      issue_s_dp<L, HD, F>(p, tmem, tmem + C_DP, pair, pairs, items, ntile, n_heads, seq, key_lens, guard);
+    mbar_wait(p.drain_bar, 0u, guard, p.abort_flag, where_code(ERR_TIMEOUT_ABWD_DRAIN, rank, 1), true);
+  } else if (warp == 2) {
     if (leader) {
+      const bool one = elect_one();
       auto where = [&](int k, int i) { return where_code(ERR_TIMEOUT_ABWD_MMA, k, i); };
-      // S(u) overwrites S(u - 1) once every warp has read it
-      auto issue_s = [&](int u, bool last) {
-        if (!qr.wait_full(u, guard, abort_flag, where(0, u)) ||
-            (u > 0 && !mbar_wait(s_empty, static_cast<uint32_t>(u - 1) & 1u, guard, abort_flag, where(1, u))))
-          return false;
-        tc_fence_after();
-        if (one) {
-          mma_rows<L, HD, F>(t_s, sK, sQr + (u % N) * L::CUT);
-          mma_commit_pair(s_full, 0x3);
-          mma_commit_pair(&qr.empty[u % N], 0x3);
-          if (last) mma_commit_pair(&kt.empty[0], 0x3);
-        }
-        __syncwarp();
-        return true;
-      };
-      // dP(u) overwrites dS(u - 1), which dK(u - 1), issued before, has read by then (in-order issue)
-      auto issue_dp = [&](int u, bool last) {
-        if (!dor.wait_full(u, guard, abort_flag, where(2, u))) return false;
-        tc_fence_after();
-        if (one) {
-          mma_rows<L, HD, F>(t_dp, sV, sOr + (u % N) * L::CUT);
-          mma_commit_pair(dp_full, 0x3);
-          mma_commit_pair(&dor.empty[u % N], 0x3);
-          if (last) mma_commit_pair(&vt.empty[0], 0x3);
-        }
-        __syncwarp();
-        return true;
-      };
       bool ok = true;
       int u = 0, ui = 0;
       for (int i = pair; i < items && ok; i += pairs) {
-        const int nb = item_of(i, ntile, n_heads, seq, key_lens, BQ).nb;
+        const int nb = item_of<R>(i, ntile, n_heads, seq, key_lens).nb;
         if (nb == 0) continue;
-        ok = kt.wait_full(ui, guard, abort_flag, where(3, u)) && issue_s(u, nb == 1) &&
-             vt.wait_full(ui, guard, abort_flag, where(4, u)) && issue_dp(u, nb == 1);
+        // the first dV of an item overwrites accumulators that both CTAs must have read
+        ok = ui == 0 || mbar_wait(p.acc_empty, static_cast<uint32_t>(ui - 1) & 1u, guard, p.abort_flag, where(5, u));
         for (int j = 0; j < nb && ok; ++j, ++u) {
-          const bool next = j + 1 < nb;
           const uint32_t par = static_cast<uint32_t>(u) & 1u;
-          // the first dV of an item overwrites accumulators that both CTAs must have read
-          ok = (!next || issue_s(u + 1, j + 2 == nb)) && doc.wait_full(u, guard, abort_flag, where(5, u)) &&
-               (j > 0 || ui == 0 ||
-                mbar_wait(acc_empty, static_cast<uint32_t>(ui - 1) & 1u, guard, abort_flag, where(6, u))) &&
-               mbar_wait(p_full, par, guard, abort_flag, where(7, u));
+          const uint8_t* slot = p.mem_b + (u % N) * L::SLOT_B;
+          ok = p.rb.wait_full(u, guard, p.abort_flag, where(6, u)) &&
+               mbar_wait(p.p_full, par, guard, p.abort_flag, where(7, u));
           if (!ok) break;
           tc_fence_after();
           if (one) {
-            mma_cols<BQ, HD, F>(t_dv, t_p, COLS / 2, sOc + (u % N) * L::CUT, j > 0);
-            mma_commit_pair(p_empty, 0x3);
-            mma_commit_pair(&doc.empty[u % N], 0x3);
+            mma_cols<L, HD, F>(tmem + C_DV, tmem + C_P, slot, j > 0);
+            mma_commit_pair(p.p_empty, 0x3);
           }
           __syncwarp();
-          ok = qc.wait_full(u, guard, abort_flag, where(8, u)) && mbar_wait(ds_full, par, guard, abort_flag, where(9, u));
+          ok = mbar_wait(p.ds_full, par, guard, p.abort_flag, where(8, u));
           if (!ok) break;
           tc_fence_after();
           if (one) {
-            mma_cols<BQ, HD, F>(t_dk, t_dp, COLS, sQc + (u % N) * L::CUT, j > 0);
-            mma_commit_pair(&qc.empty[u % N], 0x3);
+            mma_cols<L, HD, F>(tmem + C_DK, tmem + C_DS, slot + L::CUT, j > 0);
+            mma_commit_pair(p.ds_empty, 0x3);
+            mma_commit_pair(&p.rb.empty[u % N], 0x3);
           }
           __syncwarp();
-          if (next) ok = issue_dp(u + 1, j + 2 == nb);
         }
-        if (ok && one) mma_commit_pair(acc_full, 0x3);
+        if (ok && one) mma_commit_pair(p.acc_full, 0x3);
         __syncwarp();
         ++ui;
       }
-      if (one) mma_commit_pair(drain_bar, 0x3);  // all MMAs retired before either CTA frees TMEM
+      if (one) mma_commit_pair(p.drain_bar, 0x3);
       __syncwarp();
     }
-    mbar_wait(drain_bar, 0u, guard, abort_flag, where_code(ERR_TIMEOUT_ABWD_DRAIN, rank, 1), true);
+    mbar_wait(p.drain_bar, 0u, guard, p.abort_flag, where_code(ERR_TIMEOUT_ABWD_DRAIN, rank, 2), true);
   } else {
-    const int part = (warp - 2) >> 2;
+    const int part = (warp - L::FIRST_EW) >> 2;
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t s_col = t_s + lane_off + COLS * part;
-    const uint32_t dp_col = t_dp + lane_off + COLS * part;
-    const uint32_t p_col = t_p + lane_off + COLS / 2 * part;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t s_col = lanes + COLS * part, dp_col = s_col + C_DP;
+    const uint32_t p_col = lanes + C_P + COLS / 2 * part, ds_col = lanes + C_DS + COLS / 2 * part;
     const float scale = HD == 128 ? 0.08838834764831845f : 0.125f;
     const float2 c2 = make_float2(scale * LOG2E, scale * LOG2E);
     auto where = [&](int k, int i) { return where_code(ERR_TIMEOUT_ABWD_SOFTMAX, k, i); };
+    auto arrive = [&](uint64_t* bar) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(bar), 0));
+    };
     bool ok = true;
     int u = 0, ui = 0;
     for (int i = pair; i < items && ok; i += pairs) {
-      const Item it = item_of(i, ntile, n_heads, seq, key_lens, BQ);
+      const Item it = item_of<R>(i, ntile, n_heads, seq, key_lens);
       const int row0 = it.tt * 2 * T + rank * T;
       if (it.nb == 0) {
-        const int t = static_cast<int>(threadIdx.x) - 64;
+        const int t = static_cast<int>(threadIdx.x) - 32 * L::FIRST_EW;
         zero_rows<HD, 32 * L::EW_WARPS>(dk.p + static_cast<int64_t>(it.b) * seq * dk.ld + it.head * HD, dk.ld, row0, seq, t);
         zero_rows<HD, 32 * L::EW_WARPS>(dv.p + static_cast<int64_t>(it.b) * seq * dv.ld + it.head * HD, dv.ld, row0, seq, t);
         continue;
@@ -667,55 +714,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
       const float tau = F == FMT_F16 ? exp2f(shift - P_SHIFT) : 1.f;
       for (int j = 0; j < it.nb; ++j, ++u) {
         const uint32_t par = static_cast<uint32_t>(u) & 1u;
-        const int st = u % N;
-        const float* vec = sVec + st * 2 * BQ + COLS * part;
-        ok = mbar_wait(&vec_full[st], static_cast<uint32_t>(u / N) & 1u, guard, abort_flag, where(0, u)) &&
-             mbar_wait(s_full, par, guard, abort_flag, where(1, u));
+        const int sv = u % NV;
+        const float* vec = p.vec + sv * 2 * R + COLS * part;
+        ok = mbar_wait(&p.vec_full[sv], static_cast<uint32_t>(u / NV) & 1u, guard, p.abort_flag, where(0, u)) &&
+             mbar_wait(p.s_full, par, guard, p.abort_flag, where(1, u));
         if (!ok) break;
         tc_fence_after();
-        float p[COLS];
-        get_part(s_col, p);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(s_empty), 0));
+        uint32_t raw[COLS];
+        get_cols(s_col, raw);
+        got_cols(raw);
+        arrive(p.s_empty);
+        float e[COLS];
+        uint32_t pk[COLS / 2];
 #pragma unroll
         for (int k = 0; k < COLS; k += 2) {
-          const float2 l = *reinterpret_cast<const float2*>(vec + k);
-          const float2 x = fma2(make_float2(p[k], p[k + 1]), c2, make_float2(-l.x, -l.y));
-          p[k] = ex2_approx(x.x);
-          p[k + 1] = ex2_approx(x.y);
+          const float2 x = fma2(as_f2(raw + k), c2, *reinterpret_cast<const float2*>(vec + k));
+          e[k] = ex2_approx(x.x);
+          e[k + 1] = ex2_approx(x.y);
+          pk[k / 2] = pack2<F>(e[k], e[k + 1]);
         }
-        ok = mbar_wait(p_empty, par ^ 1u, guard, abort_flag, where(2, u));
+        ok = mbar_wait(p.p_empty, par ^ 1u, guard, p.abort_flag, where(2, u));  // dV(u - 1) has read P
         if (!ok) break;
         tc_fence_after();
-        put_part<F>(p_col, p);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(p_full), 0));
-        ok = mbar_wait(dp_full, par, guard, abort_flag, where(3, u));
+        put_cols(p_col, pk);
+        tmem_st_wait();
+        arrive(p.p_full);
+        ok = mbar_wait(p.dp_full, par, guard, p.abort_flag, where(3, u));
         if (!ok) break;
         tc_fence_after();
-        float x[COLS];
-        get_part(dp_col, x);
+        get_cols(dp_col, raw);
+        got_cols(raw);
+        arrive(p.dp_empty);
 #pragma unroll
         for (int k = 0; k < COLS; k += 2) {
-          const float2 dl = *reinterpret_cast<const float2*>(vec + BQ + k);
-          float2 y = add2(make_float2(x[k], x[k + 1]), make_float2(-dl.x, -dl.y));
-          y = mul2(y, make_float2(p[k], p[k + 1]));
+          float2 y = mul2(add2(as_f2(raw + k), *reinterpret_cast<const float2*>(vec + R + k)),
+                          make_float2(e[k], e[k + 1]));
           if constexpr (F == FMT_F16) y = mul2(y, make_float2(tau, tau));
-          x[k] = y.x;
-          x[k + 1] = y.y;
+          pk[k / 2] = pack2<F>(y.x, y.y);
         }
-        put_part<F>(dp_col, x);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&vec_empty[st]);
-          mbar_arrive_remote(mapa_shared(smem_u32(ds_full), 0));
-        }
+        ok = mbar_wait(p.ds_empty, par ^ 1u, guard, p.abort_flag, where(4, u));  // dK(u - 1) has read dS
+        if (!ok) break;
+        tc_fence_after();
+        put_cols(ds_col, pk);
+        tmem_st_wait();
+        arrive(p.ds_full);
       }
       if (!ok) break;
-      ok = mbar_wait(acc_full, static_cast<uint32_t>(ui) & 1u, guard, abort_flag, where(4, u));
+      ok = mbar_wait(p.acc_full, static_cast<uint32_t>(ui) & 1u, guard, p.abort_flag, where(5, u));
       if (!ok) break;
       tc_fence_after();
       {
@@ -727,70 +772,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
         for (int c = part; c < 2 * HD / 32; c += L::PARTS) {
           const bool is_v = c < HD / 32;
           const int col = 32 * (is_v ? c : c - HD / 32);
-          store_row<32, F>((is_v ? t_dv : t_dk) + lane_off + col, is_v ? fv : fk, (is_v ? dst_v : dst_k) + col, row < seq,
+          store_row<32, F>(lanes + (is_v ? C_DV : C_DK) + col, is_v ? fv : fk, (is_v ? dst_v : dst_k) + col, row < seq,
                            row < it.n);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(acc_empty), 0));
+      arrive(p.acc_empty);
       ++ui;
     }
   }
-
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();  // neither CTA leaves while the pair MMAs or remote arrives may touch it
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc_pair(tmem, TMEM_COLS);
-  }
+  finish(tmem);
 }
 
 // ------------------------------------------------------------------ dQ
 
-// The same pair of CTAs with 256 queries: S = Q K^T and dP = dO V^T per key block, dS = P (dP - delta)
-// written over S as 16-bit pairs (an A operand in TMEM), dQ += dS K.  S is double-buffered, and dP is
-// free as soon as it has been read into registers, so the products of block j + 1 run beside the
-// elementwise step of block j.  TMEM: S0 | S1 | dP | dQ.  Thread = query row and a quarter of the keys: lse
-// and delta are per thread.  K comes in both cuts, V in rows; three slots each.
+// Own rows: queries; streamed: keys in blocks of 128.  S = Q K^T and dP = dO V^T, dS = P (dP - delta) as an
+// A operand in TMEM, dQ += dS K.  TMEM: S | dP | dS (64 columns) | dQ.  lse and delta are per thread.
 struct DqMaps {
   CUtensorMap q, dout, k_rows, k_cols, v_rows, tk_rows, tk_cols;
 };
-
 template <int HD>
-using DqLayout = Layout<HD, T, 3>;
+using DqLayout = Layout<HD, DqShape>;
 
 template <int HD, int F>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DqLayout<HD>::THREADS, 1)
-    bwd_dq_kernel(const __grid_constant__ DqMaps tm, const float* __restrict__ lse2, const float* __restrict__ delta,
+    bwd_dq_kernel(const __grid_constant__ DqMaps tm, const float* __restrict__ nlse2, const float* __restrict__ ndelta,
                   const float2* __restrict__ norms2, OutRows dq, int batch, int seq, int n_heads,
                   const int32_t* __restrict__ key_lens, const KernelGuard guard) {
   using L = DqLayout<HD>;
-  constexpr int N = L::N;
+  constexpr int R = L::R, COLS = L::COLS, N = L::N;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = smem + L::OFF_A;
-  uint8_t* sDO = smem + L::OFF_B;
-  uint8_t* sKr = smem + L::OFF_RING;
-  uint8_t* sVr = sKr + N * L::CUT;
-  uint8_t* sKc = sVr + N * L::CUT;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-  const Ring<N> kr(bars), vr(bars + 2 * N), kc(bars + 4 * N);
-  const Ring<1> qt(bars + 6 * N), dt(bars + 6 * N + 2);
-  uint64_t* s_full = bars + 6 * N + 4;  // [2]
-  uint64_t* dp_full = s_full + 2;
-  uint64_t* dp_empty = dp_full + 1;     // leader: every elementwise warp of both CTAs
-  // leader: every elementwise warp of both CTAs; one per S buffer, since a warp may be done with block u + 1 (whose
-  // products do not wait for dS(u)) before another has written its dS(u)
-  uint64_t* ds_full = dp_empty + 1;     // [2]
-  uint64_t* acc_full = ds_full + 2;
-  uint64_t* acc_empty = acc_full + 1;   // leader: every elementwise warp of both CTAs
-  uint64_t* drain_bar = acc_empty + 1;
-  static_assert(6 * N + 4 + 9 <= L::NUM_BARS, "barriers fit");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
-  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::OFF_MISC + 4);
-
+  const Pipe<L, HD> p(smem, reinterpret_cast<uint64_t*>(smem + L::OFF_BAR));
   const int warp = static_cast<int>(warp_id());
   const int lane = static_cast<int>(lane_id());
   const int rank = static_cast<int>(cluster_ctarank());
@@ -799,245 +811,186 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DqLayout<HD>::THREAD
   const int nblk = blocks_of(seq) + 1;
   const int ntile = (seq + 2 * T - 1) / (2 * T);
   const int items = batch * n_heads * ntile;
-
-  if (threadIdx.x == 0) {
-    kr.init();
-    vr.init();
-    kc.init();
-    qt.init();
-    dt.init();
-    mbar_init(&s_full[0], 1);
-    mbar_init(&s_full[1], 1);
-    mbar_init(dp_full, 1);
-    mbar_init(dp_empty, 2 * L::EW_WARPS);
-    mbar_init(&ds_full[0], 2 * L::EW_WARPS);
-    mbar_init(&ds_full[1], 2 * L::EW_WARPS);
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 2 * L::EW_WARPS);
-    mbar_init(drain_bar, 1);
-    *abort_flag = 0u;
-    fence_barrier_init();
-  }
-  if (warp == 1) tmem_alloc_pair(tmem_slot, TMEM_COLS);
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const uint32_t t_dp = tmem + 256, t_dq = tmem + 384;
-  pdl_wait_then_release();
+  const uint32_t tmem = begin(p);
+  constexpr int C_DP = R, C_DS = 2 * R, C_DQ = 384;
+  static_assert(C_DS + R / 2 <= C_DQ, "TMEM columns");
+  // No wait here: this kernel reads nothing that bwd_dkv_kernel writes, and it cannot start before every
+  // CTA of that kernel has seen bwd_prep_kernel's results (they release their dependents after waiting
+  // for it).  So the SMs that finish their share of dK, dV early go on with dQ.  The wait is at the end:
+  // what follows on the stream may take this kernel's end for the end of both.
 
   if (warp == 0) {
     const bool one = elect_one();
-    int u = 0, ui = 0;
-    int n_kr = 0, n_vr = 0, n_kc = 0, n_q = 0, n_d = 0;
+    int u = 0, ui = 0, n_b = 0, n_at = 0, n_bt = 0;
     bool ok = true;
-    auto where = [&](int i) { return where_code(ERR_TIMEOUT_ABWD_PRODUCER, rank, i); };
+    auto where = [&](int i) { return where_code(ERR_TIMEOUT_ABWD_PRODUCER, 2 + rank, i); };
     for (int i = pair; i < items && ok; i += pairs) {
-      const Item it = item_of(i, ntile, n_heads, seq, key_lens, T);
+      const Item it = item_of<R>(i, ntile, n_heads, seq, key_lens);
       if (it.nb == 0) continue;
-      const bool tail = has_tail(it.n, seq, T);
+      const bool tail = has_tail(it.n, seq, R);
       const int x = it.head * HD, row0 = it.tt * 2 * T + rank * T;
-      ok = qt.wait_empty(ui, guard, abort_flag, where(0xFFFF));
+      ok = p.at.wait_empty(ui, guard, p.abort_flag, where(0xFFFF));
       if (!ok) break;
-      if (one) load_tile<L, HD>(sQ, &tm.q, qt.arm(ui, leader, 2 * L::TILE), x, row0, it.b);
-      ++n_q;
+      if (one) load_tile<L, HD>(p.tile_a, &tm.q, p.at.arm(ui, leader, 2 * L::TILE), x, row0, it.b);
+      ++n_at;
       __syncwarp();
-      for (int j = 0; j < it.nb; ++j, ++u) {
+      for (int j = 0; j < it.nb && ok; ++j) {
         const bool tl = tail && j == it.nb - 1;
-        const int st = u % N;
-        ok = kr.wait_empty(u, guard, abort_flag, where(u));
+        const int y = tl ? 0 : j * R;
+        ok = p.ra.wait_empty(u, guard, p.abort_flag, where(u));
         if (!ok) break;
-        if (one)
-          load_rows_cut<L, HD>(sKr + st * L::CUT, tl ? &tm.tk_rows : &tm.k_rows, kr.arm(u, leader, 2 * L::CUT), x,
-                            tl ? 0 : j * T, it.b, rank);
-        ++n_kr;
+        if (one) {
+          uint8_t* slot = p.mem_a + (u % N) * L::SLOT_A;
+          const uint32_t bar = p.ra.arm(u, leader, 2 * L::SLOT_A);
+          load_rows_cut<L, HD>(slot, tl ? &tm.tk_rows : &tm.k_rows, bar, x, y, it.b, rank);
+          load_rows_cut<L, HD>(slot + L::CUT, &tm.v_rows, bar, x, j * R, it.b, rank);
+        }
         __syncwarp();
+        ++u;
         if (j == 0) {
-          ok = dt.wait_empty(ui, guard, abort_flag, where(0xFFFE));
+          ok = p.bt.wait_empty(ui, guard, p.abort_flag, where(0xFFFE));
           if (!ok) break;
-          if (one) load_tile<L, HD>(sDO, &tm.dout, dt.arm(ui, leader, 2 * L::TILE), x, row0, it.b);
-          ++n_d;
+          if (one) load_tile<L, HD>(p.tile_b, &tm.dout, p.bt.arm(ui, leader, 2 * L::TILE), x, row0, it.b);
+          ++n_bt;
           __syncwarp();
         }
-        ok = vr.wait_empty(u, guard, abort_flag, where(u));
+        ok = p.rb.wait_empty(n_b, guard, p.abort_flag, where(n_b));
         if (!ok) break;
         if (one)
-          load_rows_cut<L, HD>(sVr + st * L::CUT, &tm.v_rows, vr.arm(u, leader, 2 * L::CUT), x, j * T, it.b, rank);
-        ++n_vr;
-        __syncwarp();
-        ok = kc.wait_empty(u, guard, abort_flag, where(u));
-        if (!ok) break;
-        if (one)
-          load_cols_cut<HD>(sKc + st * L::CUT, tl ? &tm.tk_cols : &tm.k_cols, kc.arm(u, leader, 2 * L::CUT), x,
-                            tl ? 0 : j * T, it.b, rank);
-        ++n_kc;
+          load_cols_cut<HD>(p.mem_b + (n_b % N) * L::SLOT_B, tl ? &tm.tk_cols : &tm.k_cols,
+                            p.rb.arm(n_b, leader, 2 * L::SLOT_B), x, y, it.b, rank);
+        ++n_b;
         __syncwarp();
       }
       ++ui;
     }
-    if (leader) {
-      const uint32_t wd = where_code(ERR_TIMEOUT_ABWD_DRAIN, 2, 0);
-      qt.drain(n_q, guard, abort_flag, wd);
-      dt.drain(n_d, guard, abort_flag, wd);
-      kr.drain(n_kr, guard, abort_flag, wd);
-      vr.drain(n_vr, guard, abort_flag, wd);
-      kc.drain(n_kc, guard, abort_flag, wd);
-    }
+    drain_loads(p, n_at, n_bt, u, n_b, 0, rank, guard);
   } else if (warp == 1) {
-    const bool one = elect_one();
+    if (leader)
+      issue_s_dp<L, HD, F>(p, tmem, tmem + C_DP, pair, pairs, items, ntile, n_heads, seq, key_lens, guard);
+    mbar_wait(p.drain_bar, 0u, guard, p.abort_flag, where_code(ERR_TIMEOUT_ABWD_DRAIN, rank, 3), true);
+  } else if (warp == 2) {
     if (leader) {
+      const bool one = elect_one();
       auto where = [&](int k, int i) { return where_code(ERR_TIMEOUT_ABWD_MMA, k, i); };
-      auto issue_s = [&](int u) {
-        mma_rows<L, HD, F>(tmem + 128 * (u & 1), sQ, sKr + (u % N) * L::CUT);
-        mma_commit_pair(&s_full[u & 1], 0x3);
-        mma_commit_pair(&kr.empty[u % N], 0x3);
-      };
-      auto issue_dp = [&](int u) {
-        mma_rows<L, HD, F>(t_dp, sDO, sVr + (u % N) * L::CUT);
-        mma_commit_pair(dp_full, 0x3);
-        mma_commit_pair(&vr.empty[u % N], 0x3);
-      };
-      // block u: S into the buffer whose dS(u - 2) was read by dQ(u - 2), issued before; dP once
-      // dP(u - 1) has been read
-      auto issue_block = [&](int u, bool last) {
-        if (!kr.wait_full(u, guard, abort_flag, where(0, u))) return false;
-        tc_fence_after();
-        if (one) {
-          issue_s(u);
-          if (last) mma_commit_pair(&qt.empty[0], 0x3);
-        }
-        __syncwarp();
-        if (!vr.wait_full(u, guard, abort_flag, where(1, u)) ||
-            (u > 0 && !mbar_wait(dp_empty, static_cast<uint32_t>(u - 1) & 1u, guard, abort_flag, where(2, u))))
-          return false;
-        tc_fence_after();
-        if (one) {
-          issue_dp(u);
-          if (last) mma_commit_pair(&dt.empty[0], 0x3);
-        }
-        __syncwarp();
-        return true;
-      };
       bool ok = true;
       int u = 0, ui = 0;
       for (int i = pair; i < items && ok; i += pairs) {
-        const int nb = item_of(i, ntile, n_heads, seq, key_lens, T).nb;
+        const int nb = item_of<R>(i, ntile, n_heads, seq, key_lens).nb;
         if (nb == 0) continue;
-        ok = qt.wait_full(ui, guard, abort_flag, where(3, u)) && dt.wait_full(ui, guard, abort_flag, where(4, u)) &&
-             issue_block(u, nb == 1);
+        // the first dQ of an item overwrites an accumulator that both CTAs must have read
+        ok = ui == 0 || mbar_wait(p.acc_empty, static_cast<uint32_t>(ui - 1) & 1u, guard, p.abort_flag, where(9, u));
         for (int j = 0; j < nb && ok; ++j, ++u) {
-          if (j + 1 < nb) ok = issue_block(u + 1, j + 2 == nb);
-          // the first dQ of an item overwrites an accumulator that both CTAs must have read
-          ok = ok && kc.wait_full(u, guard, abort_flag, where(5, u)) &&
-               mbar_wait(&ds_full[u & 1], static_cast<uint32_t>(u >> 1) & 1u, guard, abort_flag, where(6, u)) &&
-               (j > 0 || ui == 0 ||
-                mbar_wait(acc_empty, static_cast<uint32_t>(ui - 1) & 1u, guard, abort_flag, where(7, u)));
+          ok = p.rb.wait_full(u, guard, p.abort_flag, where(10, u)) &&
+               mbar_wait(p.ds_full, static_cast<uint32_t>(u) & 1u, guard, p.abort_flag, where(11, u));
           if (!ok) break;
           tc_fence_after();
           if (one) {
-            mma_cols<T, HD, F>(t_dq, tmem + 128 * (u & 1), COLS, sKc + (u % N) * L::CUT, j > 0);
-            mma_commit_pair(&kc.empty[u % N], 0x3);
+            mma_cols<L, HD, F>(tmem + C_DQ, tmem + C_DS, p.mem_b + (u % N) * L::SLOT_B, j > 0);
+            mma_commit_pair(p.ds_empty, 0x3);
+            mma_commit_pair(&p.rb.empty[u % N], 0x3);
           }
           __syncwarp();
         }
-        if (ok && one) mma_commit_pair(acc_full, 0x3);
+        if (ok && one) mma_commit_pair(p.acc_full, 0x3);
         __syncwarp();
         ++ui;
       }
-      if (one) mma_commit_pair(drain_bar, 0x3);
+      if (one) mma_commit_pair(p.drain_bar, 0x3);
       __syncwarp();
     }
-    mbar_wait(drain_bar, 0u, guard, abort_flag, where_code(ERR_TIMEOUT_ABWD_DRAIN, 3, rank), true);
+    mbar_wait(p.drain_bar, 0u, guard, p.abort_flag, where_code(ERR_TIMEOUT_ABWD_DRAIN, rank, 4), true);
   } else {
-    const int part = (warp - 2) >> 2;
+    const int part = (warp - L::FIRST_EW) >> 2;
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t dp_col = t_dp + lane_off + COLS * part;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t s_col = lanes + COLS * part, dp_col = s_col + C_DP, ds_col = lanes + C_DS + COLS / 2 * part;
     const float scale = HD == 128 ? 0.08838834764831845f : 0.125f;
     const float2 c2 = make_float2(scale * LOG2E, scale * LOG2E);
     auto where = [&](int k, int i) { return where_code(ERR_TIMEOUT_ABWD_SOFTMAX, k, i); };
+    auto arrive = [&](uint64_t* bar) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(bar), 0));
+    };
     bool ok = true;
     int u = 0, ui = 0;
     for (int i = pair; i < items && ok; i += pairs) {
-      const Item it = item_of(i, ntile, n_heads, seq, key_lens, T);
+      const Item it = item_of<R>(i, ntile, n_heads, seq, key_lens);
       const int row0 = it.tt * 2 * T + rank * T;
       if (it.nb == 0) {
         zero_rows<HD, 32 * L::EW_WARPS>(dq.p + static_cast<int64_t>(it.b) * seq * dq.ld + it.head * HD, dq.ld, row0, seq,
-                                        static_cast<int>(threadIdx.x) - 64);
+                                        static_cast<int>(threadIdx.x) - 32 * L::FIRST_EW);
         continue;
       }
       // the padded row vectors reach past the pair's 256 rows
       const int64_t at = it.bh * nblk * T + row0 + r;
-      const float l2 = lse2[at];
-      const float dl = delta[at];
+      const float nl = nlse2[at], nd = ndelta[at];
       const float shift = ds_shift<F>(norms2 + it.bh * nblk, blocks_of(it.n));
       const float tau = F == FMT_F16 ? exp2f(shift - P_SHIFT) : 1.f;
-      const float2 nl2 = make_float2(-l2, -l2);
+      const float2 nl2 = make_float2(nl, nl);
       // tau (dP - delta): one fma on the pair
-      const float2 tau2 = make_float2(tau, tau), nd2 = make_float2(-dl * tau, -dl * tau);
+      const float2 tau2 = make_float2(tau, tau), nd2 = make_float2(nd * tau, nd * tau);
       for (int j = 0; j < it.nb; ++j, ++u) {
-        const uint32_t s_col = tmem + 128 * (u & 1) + lane_off + COLS * part;
-        ok = mbar_wait(&s_full[u & 1], static_cast<uint32_t>(u >> 1) & 1u, guard, abort_flag, where(5, u));
+        const uint32_t par = static_cast<uint32_t>(u) & 1u;
+        ok = mbar_wait(p.s_full, par, guard, p.abort_flag, where(6, u));
         if (!ok) break;
         tc_fence_after();
-        float p[COLS];
-        get_part(s_col, p);
+        uint32_t raw[COLS];
+        get_cols(s_col, raw);
+        got_cols(raw);
+        arrive(p.s_empty);
+        float e[COLS];
 #pragma unroll
         for (int k = 0; k < COLS; k += 2) {
-          const float2 x = fma2(make_float2(p[k], p[k + 1]), c2, nl2);
-          p[k] = ex2_approx(x.x);
-          p[k + 1] = ex2_approx(x.y);
+          const float2 x = fma2(as_f2(raw + k), c2, nl2);
+          e[k] = ex2_approx(x.x);
+          e[k + 1] = ex2_approx(x.y);
         }
-        ok = mbar_wait(dp_full, static_cast<uint32_t>(u) & 1u, guard, abort_flag, where(6, u));
+        ok = mbar_wait(p.dp_full, par, guard, p.abort_flag, where(7, u));
         if (!ok) break;
         tc_fence_after();
-        float x[COLS];
-        get_part(dp_col, x);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(dp_empty), 0));
-#pragma unroll
-        for (int k = 0; k < COLS; k += 2) {
-          float2 y = F == FMT_F16 ? fma2(make_float2(x[k], x[k + 1]), tau2, nd2) : add2(make_float2(x[k], x[k + 1]), nd2);
-          y = mul2(y, make_float2(p[k], p[k + 1]));
-          x[k] = y.x;
-          x[k + 1] = y.y;
-        }
-        const int valid = it.n - j * T - COLS * part;  // keys past the tokens: dS = 0 whatever S and dP hold
+        get_cols(dp_col, raw);
+        got_cols(raw);
+        arrive(p.dp_empty);
+        const int valid = it.n - j * R - COLS * part;  // keys past the tokens: dS = 0 whatever S and dP hold
         if (valid < COLS) {
 #pragma unroll
-          for (int k = 0; k < COLS; ++k) x[k] = k < valid ? x[k] : 0.f;
+          for (int k = 0; k < COLS; ++k) {
+            e[k] = k < valid ? e[k] : 0.f;
+            raw[k] = k < valid ? raw[k] : 0u;
+          }
         }
-        put_part<F>(s_col, x);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&ds_full[u & 1]), 0));
+        uint32_t pk[COLS / 2];
+#pragma unroll
+        for (int k = 0; k < COLS; k += 2) {
+          const float2 v = as_f2(raw + k);
+          const float2 y = mul2(F == FMT_F16 ? fma2(v, tau2, nd2) : add2(v, nd2), make_float2(e[k], e[k + 1]));
+          pk[k / 2] = pack2<F>(y.x, y.y);
+        }
+        ok = mbar_wait(p.ds_empty, par ^ 1u, guard, p.abort_flag, where(8, u));  // dQ(u - 1) has read dS
+        if (!ok) break;
+        tc_fence_after();
+        put_cols(ds_col, pk);
+        tmem_st_wait();
+        arrive(p.ds_full);
       }
       if (!ok) break;
-      ok = mbar_wait(acc_full, static_cast<uint32_t>(ui) & 1u, guard, abort_flag, where(7, u));
+      ok = mbar_wait(p.acc_full, static_cast<uint32_t>(ui) & 1u, guard, p.abort_flag, where(9, u));
       if (!ok) break;
       tc_fence_after();
       const int row = row0 + r;
       if (part < HD / 32)
-        store_row<32, F>(t_dq + lane_off + 32 * part, scale * exp2f(-shift),
+        store_row<32, F>(lanes + C_DQ + 32 * part, scale * exp2f(-shift),
                          dq.p + (static_cast<int64_t>(it.b) * seq + row) * dq.ld + it.head * HD + 32 * part, row < seq,
                          row < it.n);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(acc_empty), 0));
+      arrive(p.acc_empty);
       ++ui;
     }
   }
-
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc_pair(tmem, TMEM_COLS);
-  }
+  finish(tmem);
+  pdl_wait_then_release();
 }
 
 // ------------------------------------------------------------------ launch
@@ -1072,16 +1025,16 @@ static cudaError_t launch_hd(Rows q, Rows k, Rows v, const void* out, const void
   DqMaps mq;
   tile(&mq.q, q);
   tile(&mq.dout, go);
-  cuts(&mq.k_rows, &mq.k_cols, k, seq, T);
-  cuts(&mq.v_rows, nullptr, v, seq, T);
-  cuts(&mq.tk_rows, &mq.tk_cols, tk, T, T);
+  cuts(&mq.k_rows, &mq.k_cols, k, seq, LQ::R);
+  cuts(&mq.v_rows, nullptr, v, seq, LQ::R);
+  cuts(&mq.tk_rows, &mq.tk_cols, tk, T, LQ::R);
   DkvMaps mk;
   tile(&mk.k, k);
   tile(&mk.v, v);
-  cuts(&mk.q_rows, &mk.q_cols, q, seq, BQ);
-  cuts(&mk.do_rows, &mk.do_cols, go, seq, BQ);
-  cuts(&mk.tq_rows, &mk.tq_cols, tq, T, BQ);
-  cuts(&mk.tdo_rows, &mk.tdo_cols, tdo, T, BQ);
+  cuts(&mk.q_rows, &mk.q_cols, q, seq, LK::R);
+  cuts(&mk.do_rows, &mk.do_cols, go, seq, LK::R);
+  cuts(&mk.tq_rows, &mk.tq_cols, tq, T, LK::R);
+  cuts(&mk.tdo_rows, &mk.tdo_cols, tdo, T, LK::R);
   if (!ok) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(bwd_dkv_kernel<HD, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, LK::SMEM);
   if (e == cudaSuccess)
@@ -1089,7 +1042,7 @@ static cudaError_t launch_hd(Rows q, Rows k, Rows v, const void* out, const void
   if (e != cudaSuccess) return e;
   const PrepArgs pa{static_cast<const uint16_t*>(q.p), static_cast<const uint16_t*>(k.p),
                     static_cast<const uint16_t*>(v.p), static_cast<const uint16_t*>(out),
-                    static_cast<const uint16_t*>(dout), q.ld, k.ld, v.ld, lse, key_lens, w.lse2, w.delta, w.norms2,
+                    static_cast<const uint16_t*>(dout), q.ld, k.ld, v.ld, lse, key_lens, w.nlse2, w.ndelta, w.norms2,
                     w.tails, batch, seq, n_heads};
   e = launch_pdl(bwd_prep_kernel<HD, F>, dim3(nblk, n_heads, batch), dim3(256), 0, s, pa);
   if (e != cudaSuccess) return e;
@@ -1099,11 +1052,11 @@ static cudaError_t launch_hd(Rows q, Rows k, Rows v, const void* out, const void
   const int64_t items = static_cast<int64_t>((seq + 2 * T - 1) / (2 * T)) * n_heads * batch;
   const dim3 grid(2u * static_cast<unsigned>(items < sms / 2 ? items : sms / 2));
   auto view = [](Rows r) { return OutRows{static_cast<uint16_t*>(const_cast<void*>(r.p)), r.ld}; };
-  e = launch_pdl(bwd_dq_kernel<HD, F>, grid, dim3(LQ::THREADS), LQ::SMEM, s, mq, w.lse2, w.delta, w.norms2, view(dq), batch,
-                 seq, n_heads, key_lens, g);
+  e = launch_pdl(bwd_dkv_kernel<HD, F>, grid, dim3(LK::THREADS), LK::SMEM, s, mk, w.nlse2, w.ndelta, w.norms2, view(dk),
+                 view(dv), batch, seq, n_heads, key_lens, g);
   if (e != cudaSuccess) return e;
-  return launch_pdl(bwd_dkv_kernel<HD, F>, grid, dim3(LK::THREADS), LK::SMEM, s, mk, w.lse2, w.delta, w.norms2, view(dk),
-                    view(dv), batch, seq, n_heads, key_lens, g);
+  return launch_pdl(bwd_dq_kernel<HD, F>, grid, dim3(LQ::THREADS), LQ::SMEM, s, mq, w.nlse2, w.ndelta, w.norms2, view(dq),
+                    batch, seq, n_heads, key_lens, g);
 }
 
 }  // namespace abwd
