@@ -37,11 +37,12 @@ constexpr float P_SHIFT = 15.f;  // f16: P is held as 2^15 P
 
 // The shape of one pass: blocks of R rows of the streamed axis, COLS of them per elementwise thread (a
 // warp works on a 32 x COLS piece), SLOTS blocks of operands in flight.
+// OUT columns of an accumulator are staged per warp for the store; VECS slots of row vectors.
 struct DkvShape {
-  static constexpr int R = 80, COLS = 16, SLOTS = 3, CUTS_B = 2;
+  static constexpr int R = 80, COLS = 16, SLOTS = 3, CUTS_B = 2, OUT = 32, VECS = 5;
 };
 struct DqShape {
-  static constexpr int R = 128, COLS = 32, SLOTS = 3, CUTS_B = 1;
+  static constexpr int R = 128, COLS = 32, SLOTS = 3, CUTS_B = 1, OUT = 16, VECS = 0;
 };
 
 __host__ __device__ inline int blocks_of(int seq) { return (seq + T - 1) / T; }
@@ -218,7 +219,7 @@ struct Layout {
   static constexpr int EW_WARPS = 4 * PARTS;
   static constexpr int FIRST_EW = 3;  // after the loading and the two issuing warps
   static constexpr int THREADS = 32 * (FIRST_EW + EW_WARPS);
-  static constexpr int NV = 5;  // slots of the row vectors (dkv)
+  static constexpr int NV = Shape::VECS, OUT = Shape::OUT;
   static constexpr int SLAB = T * 128;
   static constexpr int TILE = (HD / 64) * SLAB;
   static constexpr int RSLAB = R / 2 * 128;
@@ -229,13 +230,16 @@ struct Layout {
   static constexpr int OFF_RING_A = OFF_B + TILE;
   static constexpr int OFF_RING_B = OFF_RING_A + N * SLOT_A;
   static constexpr int OFF_VEC = OFF_RING_B + N * SLOT_B;  // dkv: [NV][nlse2 | ndelta], R each
-  static constexpr int OFF_BAR = OFF_VEC + NV * 2 * R * 4;
+  static constexpr int OUT_PARTS = PARTS < 4 ? PARTS : 4;  // parts that store
+  static constexpr int OFF_OUT = OFF_VEC + NV * 2 * R * 4;  // [4 OUT_PARTS warps][32 rows][OUT]
+  static constexpr int OFF_BAR = OFF_OUT + 4 * OUT_PARTS * 32 * OUT * 2;
   static constexpr int NUM_BARS = 4 * N + 4 + NV + 11;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static_assert(SMEM <= 232448, "227 KB of shared memory per CTA");
   static_assert(RSLAB % 1024 == 0 && CUT % 1024 == 0, "swizzled tiles keep their alignment");
-  static_assert(R % 16 == 0 && R % COLS == 0 && OFF_VEC % 16 == 0 && (R * 4) % 16 == 0, "");
+  static_assert(R % 16 == 0 && R % COLS == 0 && OFF_VEC % 16 == 0 && (R * 4) % 16 == 0, "bulk copies");
+  static_assert(OFF_OUT % 128 == 0 && (32 * OUT * 2) % 128 == 0, "staged pieces are TMA boxes");
 };
 
 // Global -> shared copy of a multiple of 16 bytes, both addresses 16-byte aligned.
@@ -320,21 +324,37 @@ __device__ __forceinline__ float2 as_f2(const uint32_t* r) {
   return make_float2(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-// NC columns of one accumulator row (fp32 at taddr) times f into a 16-bit row, or zeros.
-template <int NC, int F>
-__device__ __forceinline__ void store_row(uint32_t taddr, float f, uint16_t* dst, bool in_range, bool live) {
-  uint32_t raw[NC];
+// OUT columns of this warp's 32 accumulator rows (fp32 at taddr) times f, rounded to 16 bits, staged in
+// shared memory and stored as one TMA box (x, y) of element z; rows that take no part as zeros, rows past
+// the sequence are cut off by the tensor map.  Stored from registers, a row per lane, the same tiles
+// took 7000 clocks a work item of 100,000.
+template <int OUT, int F>
+__device__ __forceinline__ void store_box(const CUtensorMap* m, uint8_t* stage, uint32_t taddr, float f, bool live,
+                                          int x, int y, int z) {
+  uint32_t raw[OUT];
   get_cols(taddr, raw);
+  bulk_wait_group_read<0>();  // lane 0's previous box has left the buffer
+  __syncwarp();
   got_cols(raw);
-  if (in_range) {
 #pragma unroll
-    for (int q = 0; q < NC / 8; ++q) {
-      float o[8];
+  for (int q = 0; q < OUT / 8; ++q) {
+    float o[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = live ? __uint_as_float(raw[8 * q + k]) * f : 0.f;
-      store8<F>(dst, q, o);
-    }
+    for (int k = 0; k < 8; ++k) o[k] = live ? __uint_as_float(raw[8 * q + k]) * f : 0.f;
+    store8<F>(stage + lane_id() * (2 * OUT), q, o);
   }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane_id() == 0) {
+    tma_store_3d(m, stage, x, y, z);
+    bulk_commit_group();
+  }
+  __syncwarp();
+}
+
+template <int N>
+__device__ __forceinline__ void bulk_wait_group() {
+  asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Zeros into this CTA's 128 rows from row0, those below seq, of one head; t: index among the N
@@ -348,6 +368,7 @@ __device__ __forceinline__ void zero_rows(uint16_t* base, int64_t ld, int row0, 
   }
 }
 
+// A gradient: its rows (for zeros), and the map of its boxes of 32 rows.
 struct OutRows {
   uint16_t* p;
   int64_t ld;
@@ -535,8 +556,10 @@ template <class L, int HD>
 __device__ __forceinline__ void drain_loads(const Pipe<L, HD>& p, int n_at, int n_bt, int n_a, int n_b, int n_vec,
                                             int rank, const KernelGuard& guard) {
   const uint32_t wd = where_code(ERR_TIMEOUT_ABWD_DRAIN, rank, 0);
-  for (int v = n_vec > L::NV ? n_vec - L::NV : 0; v < n_vec; ++v)
-    mbar_wait(&p.vec_full[v % L::NV], static_cast<uint32_t>(v / L::NV) & 1u, guard, p.abort_flag, wd, true);
+  if constexpr (L::NV > 0) {
+    for (int v = n_vec > L::NV ? n_vec - L::NV : 0; v < n_vec; ++v)
+      mbar_wait(&p.vec_full[v % L::NV], static_cast<uint32_t>(v / L::NV) & 1u, guard, p.abort_flag, wd, true);
+  }
   if (rank == 0) {
     p.at.drain(n_at, guard, p.abort_flag, wd);
     p.bt.drain(n_bt, guard, p.abort_flag, wd);
@@ -555,7 +578,7 @@ __device__ __forceinline__ void drain_loads(const Pipe<L, HD>& p, int n_at, int 
 // dV(j) and dP(j+1) for dK(j): 3420 clocks a block against the products' 2048; with 96 and only
 // dS^T over dP^T 2030 against 1536.
 struct DkvMaps {
-  CUtensorMap k, v, q_rows, q_cols, do_rows, do_cols, tq_rows, tq_cols, tdo_rows, tdo_cols;
+  CUtensorMap k, v, q_rows, q_cols, do_rows, do_cols, tq_rows, tq_cols, tdo_rows, tdo_cols, dk, dv;
 };
 template <int HD>
 using DkvLayout = Layout<HD, DkvShape>;
@@ -686,7 +709,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
   } else {
     const int part = (warp - L::FIRST_EW) >> 2;
     const int quarter = warp & 3;
-    const int r = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t s_col = lanes + COLS * part, dp_col = s_col + C_DP;
     const uint32_t p_col = lanes + C_P + COLS / 2 * part, ds_col = lanes + C_DS + COLS / 2 * part;
@@ -698,18 +720,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(bar), 0));
     };
+    uint8_t* stage = smem + L::OFF_OUT + (warp - L::FIRST_EW) * 32 * L::OUT * 2;
+    auto shift_of = [&](int i) {
+      if (F != FMT_F16 || i >= items) return 0.f;
+      const Item it = item_of<R>(i, ntile, n_heads, seq, key_lens);
+      return ds_shift<F>(norms2 + it.bh * nblk, blocks_of(it.n));
+    };
     bool ok = true;
     int u = 0, ui = 0;
+    float shift = shift_of(pair);
     for (int i = pair; i < items && ok; i += pairs) {
       const Item it = item_of<R>(i, ntile, n_heads, seq, key_lens);
       const int row0 = it.tt * 2 * T + rank * T;
       if (it.nb == 0) {
+        shift = shift_of(i + pairs);
         const int t = static_cast<int>(threadIdx.x) - 32 * L::FIRST_EW;
         zero_rows<HD, 32 * L::EW_WARPS>(dk.p + static_cast<int64_t>(it.b) * seq * dk.ld + it.head * HD, dk.ld, row0, seq, t);
         zero_rows<HD, 32 * L::EW_WARPS>(dv.p + static_cast<int64_t>(it.b) * seq * dv.ld + it.head * HD, dv.ld, row0, seq, t);
         continue;
       }
-      const float shift = ds_shift<F>(norms2 + it.bh * nblk, blocks_of(it.n));
       // P carries 2^15 in f16; dS = that P times (dP - delta) times tau = 2^(shift - 15)
       const float tau = F == FMT_F16 ? exp2f(shift - P_SHIFT) : 1.f;
       for (int j = 0; j < it.nb; ++j, ++u) {
@@ -760,25 +789,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
         arrive(p.ds_full);
       }
       if (!ok) break;
+      const float fv = F == FMT_F16 ? exp2f(-P_SHIFT) : 1.f, fk = scale * exp2f(-shift);
+      shift = shift_of(i + pairs);  // the next item's, while the last products run
       ok = mbar_wait(p.acc_full, static_cast<uint32_t>(ui) & 1u, guard, p.abort_flag, where(5, u));
       if (!ok) break;
       tc_fence_after();
-      {
-        // 2 HD / 32 pieces of 32 columns (dV's, then dK's), dealt to the row's warps in turn
-        const int row = row0 + r;
-        uint16_t* dst_v = dv.p + (static_cast<int64_t>(it.b) * seq + row) * dv.ld + it.head * HD;
-        uint16_t* dst_k = dk.p + (static_cast<int64_t>(it.b) * seq + row) * dk.ld + it.head * HD;
-        const float fv = F == FMT_F16 ? exp2f(-P_SHIFT) : 1.f, fk = scale * exp2f(-shift);
-        for (int c = part; c < 2 * HD / 32; c += L::PARTS) {
-          const bool is_v = c < HD / 32;
-          const int col = 32 * (is_v ? c : c - HD / 32);
-          store_row<32, F>(lanes + (is_v ? C_DV : C_DK) + col, is_v ? fv : fk, (is_v ? dst_v : dst_k) + col, row < seq,
-                           row < it.n);
-        }
+      // 2 HD / OUT pieces of the rows (dV's, then dK's), dealt to the rows' warps in turn
+      const int row = row0 + 32 * quarter;
+      for (int c = part; part < L::OUT_PARTS && c < 2 * HD / L::OUT; c += L::OUT_PARTS) {
+        const bool is_v = c < HD / L::OUT;
+        const int col = L::OUT * (is_v ? c : c - HD / L::OUT);
+        store_box<L::OUT, F>(is_v ? &tm.dv : &tm.dk, stage, lanes + (is_v ? C_DV : C_DK) + col, is_v ? fv : fk,
+                             row + lane < it.n, it.head * HD + col, row, it.b);
       }
       arrive(p.acc_empty);
       ++ui;
     }
+    bulk_wait_group<0>();  // the last boxes are in memory
   }
   finish(tmem);
 }
@@ -788,7 +815,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
 // Own rows: queries; streamed: keys in blocks of 128.  S = Q K^T and dP = dO V^T, dS = P (dP - delta) as an
 // A operand in TMEM, dQ += dS K.  TMEM: S | dP | dS (64 columns) | dQ.  lse and delta are per thread.
 struct DqMaps {
-  CUtensorMap q, dout, k_rows, k_cols, v_rows, tk_rows, tk_cols;
+  CUtensorMap q, dout, k_rows, k_cols, v_rows, tk_rows, tk_cols, dq;
 };
 template <int HD>
 using DqLayout = Layout<HD, DqShape>;
@@ -914,20 +941,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DqLayout<HD>::THREAD
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(bar), 0));
     };
+    uint8_t* stage = smem + L::OFF_OUT + (warp - L::FIRST_EW) * 32 * L::OUT * 2;
+    struct RowState {
+      float nl, nd, shift;
+    };
+    // the padded row vectors reach past the pair's 256 rows
+    auto state_of = [&](int i) {
+      RowState s{0.f, 0.f, 0.f};
+      if (i >= items) return s;
+      const Item it = item_of<R>(i, ntile, n_heads, seq, key_lens);
+      const int64_t at = it.bh * nblk * T + it.tt * 2 * T + rank * T + r;
+      s.nl = nlse2[at];
+      s.nd = ndelta[at];
+      s.shift = ds_shift<F>(norms2 + it.bh * nblk, blocks_of(it.n));
+      return s;
+    };
     bool ok = true;
     int u = 0, ui = 0;
+    RowState next = state_of(pair);
     for (int i = pair; i < items && ok; i += pairs) {
       const Item it = item_of<R>(i, ntile, n_heads, seq, key_lens);
       const int row0 = it.tt * 2 * T + rank * T;
       if (it.nb == 0) {
+        next = state_of(i + pairs);
         zero_rows<HD, 32 * L::EW_WARPS>(dq.p + static_cast<int64_t>(it.b) * seq * dq.ld + it.head * HD, dq.ld, row0, seq,
                                         static_cast<int>(threadIdx.x) - 32 * L::FIRST_EW);
         continue;
       }
-      // the padded row vectors reach past the pair's 256 rows
-      const int64_t at = it.bh * nblk * T + row0 + r;
-      const float nl = nlse2[at], nd = ndelta[at];
-      const float shift = ds_shift<F>(norms2 + it.bh * nblk, blocks_of(it.n));
+      const float nl = next.nl, nd = next.nd, shift = next.shift;
       const float tau = F == FMT_F16 ? exp2f(shift - P_SHIFT) : 1.f;
       const float2 nl2 = make_float2(nl, nl);
       // tau (dP - delta): one fma on the pair
@@ -977,17 +1018,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DqLayout<HD>::THREAD
         arrive(p.ds_full);
       }
       if (!ok) break;
+      next = state_of(i + pairs);  // while the last products run
       ok = mbar_wait(p.acc_full, static_cast<uint32_t>(ui) & 1u, guard, p.abort_flag, where(9, u));
       if (!ok) break;
       tc_fence_after();
-      const int row = row0 + r;
-      if (part < HD / 32)
-        store_row<32, F>(lanes + C_DQ + 32 * part, scale * exp2f(-shift),
-                         dq.p + (static_cast<int64_t>(it.b) * seq + row) * dq.ld + it.head * HD + 32 * part, row < seq,
-                         row < it.n);
+      const float fq = scale * exp2f(-shift);
+      const int row = row0 + 32 * quarter;
+      for (int c = part; part < L::OUT_PARTS && c < HD / L::OUT; c += L::OUT_PARTS)
+        store_box<L::OUT, F>(&tm.dq, stage, lanes + C_DQ + L::OUT * c, fq, row + lane < it.n, it.head * HD + L::OUT * c,
+                             row, it.b);
       arrive(p.acc_empty);
       ++ui;
     }
+    bulk_wait_group<0>();  // the last boxes are in memory
   }
   finish(tmem);
   pdl_wait_then_release();
@@ -996,13 +1039,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DqLayout<HD>::THREAD
 // ------------------------------------------------------------------ launch
 
 static bool map_rows(CUtensorMap* m, int fmt, const void* p, int64_t ld, int rows, int batch, int cols, int box_cols,
-                     int box_rows) {
+                     int box_rows, bool plain = false) {
   const uint64_t dims[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows), static_cast<uint64_t>(batch)};
   const uint64_t strides[2] = {static_cast<uint64_t>(ld) * 2, static_cast<uint64_t>(rows) * ld * 2};
   const uint32_t box[3] = {static_cast<uint32_t>(box_cols), static_cast<uint32_t>(box_rows), 1};
   return make_tmap(m, fmt == FMT_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                    const_cast<void*>(p), dims, strides, box,
-                   box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+                   plain            ? CU_TENSOR_MAP_SWIZZLE_NONE
+                   : box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                    : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int HD, int F>
@@ -1035,6 +1080,11 @@ static cudaError_t launch_hd(Rows q, Rows k, Rows v, const void* out, const void
   cuts(&mk.do_rows, &mk.do_cols, go, seq, LK::R);
   cuts(&mk.tq_rows, &mk.tq_cols, tq, T, LK::R);
   cuts(&mk.tdo_rows, &mk.tdo_cols, tdo, T, LK::R);
+  // boxes of 32 rows x OUT columns, unswizzled
+  auto out_map = [&](CUtensorMap* m, Rows r, int cols) { ok = ok && map_rows(m, F, r.p, r.ld, seq, batch, d, cols, 32, true); };
+  out_map(&mq.dq, dq, LQ::OUT);
+  out_map(&mk.dk, dk, LK::OUT);
+  out_map(&mk.dv, dv, LK::OUT);
   if (!ok) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(bwd_dkv_kernel<HD, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, LK::SMEM);
   if (e == cudaSuccess)
