@@ -377,13 +377,17 @@ _FMT_DTYPES = {FMT_BF16: (torch.bfloat16, torch.int16, torch.uint16), FMT_F16: (
 
 def _on_device(**tensors) -> None:
     """Every tensor is in the current device's memory (the library runs on the current device)."""
+    dev = -2
     for name, t in tensors.items():
         if t is None:
             continue
-        if not t.is_cuda:
+        at = t.get_device()  # -1: host memory
+        if at < 0:
             raise ValueError(f"{name} must be a CUDA tensor")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+        if dev == -2:
+            dev = torch.cuda.current_device()
+        if at != dev:
+            raise ValueError(f"{name} is on cuda:{at}, the current device is cuda:{dev}")
 
 
 def _of(name: str, t: Optional[torch.Tensor], shape, dtypes) -> None:
@@ -391,7 +395,7 @@ def _of(name: str, t: Optional[torch.Tensor], shape, dtypes) -> None:
         return
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -401,11 +405,10 @@ def _rows(name: str, t: torch.Tensor, batch: int, seq: int, cols: int, fmt: int)
     if fmt not in (FMT_BF16, FMT_F16):
         raise ValueError(f"fmt {fmt} is not a 16-bit format")
     _of(name, t, (batch, seq, cols), _FMT_DTYPES[fmt])
-    if seq > 1:
-        ld = t.stride(1)
-    else:
-        ld = t.stride(0) if batch > 1 else -(-cols // 8) * 8
-    if t.stride(2) != 1 or (batch > 1 and t.stride(0) != seq * ld):
+    s0, ld, s2 = t.stride()
+    if seq == 1:
+        ld = s0 if batch > 1 else -(-cols // 8) * 8
+    if s2 != 1 or (batch > 1 and s0 != seq * ld):
         raise ValueError(f"{name} has strides {t.stride()}: columns must be adjacent and elements seq rows apart")
     return t.data_ptr(), ld
 

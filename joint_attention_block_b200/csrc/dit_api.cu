@@ -769,7 +769,7 @@ int dit_qknorm_mrope_out(const void* qkv, void* qk, int fmt, int batch, int n_te
 
 size_t dit_qknorm_mrope_backward_workspace_bytes(const dit_block_config* cfg, int batch, int seq) {
   if (check_config(cfg) != DIT_OK || batch <= 0 || seq <= 0) return 0;
-  return align256(qknorm_mrope_bwd_workspace(static_cast<int64_t>(batch) * seq, cfg->head_dim));
+  return align256(qknorm_mrope_bwd_workspace(static_cast<int64_t>(batch) * seq, cfg->n_heads, cfg->head_dim));
 }
 
 int dit_qknorm_mrope_backward(const void* qkv, const void* dqk, int64_t ld_dqk, void* dx, int64_t ld_dx, float* dg_q,
@@ -790,11 +790,13 @@ int dit_qknorm_mrope_backward(const void* qkv, const void* dqk, int64_t ld_dqk, 
   if (!aligned16(qkv) || !aligned16(g_q) || !aligned16(g_k)) return DIT_ERR_INVALID_ARG;
   const int S = n_text + grid_h * grid_w;
   if (!ws_ok(workspace, ws_bytes, dit_qknorm_mrope_backward_workspace_bytes(cfg, batch, S))) return DIT_ERR_WORKSPACE;
+  KernelGuard g;
+  if (current_guard(&g) != cudaSuccess) return DIT_ERR_CUDA;
   return from_cuda(launch_qknorm_mrope_bwd(qkv, Rows{dqk, ld_dqk}, Rows{dx, ld_dx}, dg_q, dg_k, fmt, batch, S,
                                            cfg->n_heads, cfg->head_dim, n_text, grid_w, grid_h * grid_w, t_img, pos,
                                            text_lens, cfg->rope_sections, cfg->rope_theta,
                                            static_cast<const uint16_t*>(g_q), static_cast<const uint16_t*>(g_k),
-                                           cfg->eps, workspace, as_stream(stream)));
+                                           cfg->eps, workspace, g, as_stream(stream)));
 }
 
 size_t dit_joint_attention_lse_workspace_bytes(int batch, int seq, int n_heads, int head_dim) {
@@ -872,8 +874,10 @@ int dit_rmsnorm_rows_backward(const void* x, int x_fmt, const void* g, const voi
   if (x == nullptr || g == nullptr || dy == nullptr || dx == nullptr || dx == x || dx == dy) return DIT_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(g) || !aligned16(dy) || !aligned16(dres) || !aligned16(dx)) return DIT_ERR_INVALID_ARG;
   if (!ws_ok(workspace, ws_bytes, dit_rmsnorm_rows_backward_workspace_bytes(rows, cols))) return DIT_ERR_WORKSPACE;
+  KernelGuard guard;
+  if (current_guard(&guard) != cudaSuccess) return DIT_ERR_CUDA;
   return from_cuda(launch_rmsnorm_bwd(x, x_fmt, static_cast<const uint16_t*>(g), dy, dy_fmt, dres, dx, dx_fmt, dg,
-                                      rows, cols, eps, workspace, as_stream(stream)));
+                                      rows, cols, eps, workspace, guard, as_stream(stream)));
 }
 
 }  // extern "C"

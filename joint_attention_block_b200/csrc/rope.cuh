@@ -51,6 +51,11 @@ __device__ __forceinline__ void token_position(int s, int n_text, int grid_w, in
   }
 }
 
+// Tokens of element b that take part.
+__device__ __forceinline__ int rope_count(const RopeArgs& ra, int b) {
+  return (ra.text_lens != nullptr ? min(max(ra.text_lens[b], 0), ra.n_text) : ra.n_text) + ra.n_img;
+}
+
 // Position of token s of element b; returns the number of tokens of the element that take part
 // (padding rows beyond it sit at (0, 0, 0)).
 __device__ __forceinline__ int rope_position(const RopeArgs& ra, int b, int s, int& pt, int& ph, int& pw) {

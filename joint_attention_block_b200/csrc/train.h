@@ -17,6 +17,8 @@ enum : uint32_t {
   ERR_TIMEOUT_ABWD_MMA = 0x122,
   ERR_TIMEOUT_ABWD_SOFTMAX = 0x123,
   ERR_TIMEOUT_ABWD_DRAIN = 0x124,
+  ERR_TIMEOUT_QKBWD = 0x125,
+  ERR_TIMEOUT_NORMBWD = 0x126,
 };
 
 // 16-bit [B, S, n_heads * head_dim] view: row stride ld elements, batch stride S * ld.
@@ -54,18 +56,18 @@ cudaError_t launch_qknorm_mrope_out(const void* qkv, void* qk, int fmt, int batc
 
 // Its gradient: dqk ([B, S, >= 2d] rows) is the gradient of the rotated q and k, dx (same shape, may
 // be dqk itself) receives that of the raw ones, dg_q / dg_k (fp32 [hd]) the gains'.
-size_t qknorm_mrope_bwd_workspace(int64_t tokens, int head_dim);
+size_t qknorm_mrope_bwd_workspace(int64_t tokens, int n_heads, int head_dim);
 cudaError_t launch_qknorm_mrope_bwd(const void* qkv, Rows dqk, Rows dx, float* dg_q, float* dg_k, int fmt, int batch,
                                     int seq, int n_heads, int head_dim, int n_text, int grid_w, int n_img, int t_img,
                                     const int32_t* pos, const int32_t* text_lens, const int32_t sections[3],
                                     float theta, const uint16_t* g_q, const uint16_t* g_k, float eps, void* workspace,
-                                    cudaStream_t s);
+                                    const KernelGuard& guard, cudaStream_t s);
 
 // The gradient of launch_rmsnorm: dx = (d/dx)(dy) + dres (dres NULL: none; same format as dx, may be
 // dx itself), dg fp32 [cols].  cols % 8 == 0, cols <= 8192.
 size_t rmsnorm_bwd_workspace(int64_t rows, int64_t cols);
 cudaError_t launch_rmsnorm_bwd(const void* x, int x_fmt, const uint16_t* g, const void* dy, int dy_fmt,
                                const void* dres, void* dx, int dx_fmt, float* dg, int64_t rows, int64_t cols,
-                               float eps, void* workspace, cudaStream_t s);
+                               float eps, void* workspace, const KernelGuard& guard, cudaStream_t s);
 
 }  // namespace jab

@@ -2,6 +2,8 @@
 // gains' gradients.  fp32 math.  The sums are taken in a fixed order (registers over a CTA's
 // tokens or rows, then shared memory, then one partial row per CTA that a second kernel adds up), so
 // a result does not change from run to run.
+#include <type_traits>
+
 #include "common.cuh"
 #include "rope.cuh"
 #include "train.h"
@@ -9,7 +11,7 @@
 namespace jab {
 namespace tew {
 
-constexpr int MAX_CTAS = 296;  // two per SM: what the workspaces hold a partial row for
+constexpr int SMS = 148;  // grids are multiples of it; the workspaces hold a partial row per CTA
 
 // dst[c] = sum over the n rows of part [n, cols]; one CTA per 32 columns, 32 row lanes each.
 __global__ void __launch_bounds__(1024) sum_rows_kernel(const float* __restrict__ part, int n, int64_t cols,
@@ -40,202 +42,353 @@ static cudaError_t sum_rows(const float* part, int n, int64_t cols, float* dst0,
                     dst0, dst1, split);
 }
 
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+constexpr int MAX_STAGES = 8;
+constexpr int CTAS_PER_SM = 2;  // of the QK-norm gradient up to 256 threads a token
+
+// (b, s) of the tokens blockIdx.x, blockIdx.x + gridDim.x, ... without a division for each.
+struct TokenWalk {
+  int b, s, db, ds;
+  __device__ __forceinline__ TokenWalk(int seq)
+      : b(blockIdx.x / seq), s(blockIdx.x % seq), db(gridDim.x / seq), ds(gridDim.x % seq) {}
+  __device__ __forceinline__ void step(int seq) {
+    b += db;
+    s += ds;
+    if (s >= seq) {
+      s -= seq;
+      ++b;
+    }
+  }
+};
+
 // ------------------------------------------------------------------ QK-RMSNorm + M-RoPE
 
 // With x a raw head vector, r = (mean x^2 + eps)^(-1/2), xh = r x, u = xh g and y = R u (R the
 // token's rotation of the pairs (i, i + hd/2)): dz = R^T dy, dg = sum dz xh, du = dz g and
 // dx = r (du - xh mean(du xh)).
-// Thread layout as in the forward kernel (one thread per head and 8 rotary pairs, q and k); each
-// CTA walks tokens with the gains' sums in registers, the next token's vectors loaded and its
-// angles computed (the other of two shared buffers) before the current token's arithmetic.
+// A CTA works on q or on k (blockIdx.y) and walks tokens with the gain's sums in registers (q and k
+// together needed more registers than two CTAs of an SM have); thread layout as in the forward kernel,
+// one thread per head and 8 rotary pairs.  The last warp runs ahead: it copies a token's raw rows and
+// gradients into a ring of shared memory with two bulk copies and computes its angles beside them, so
+// that the other warps wait for neither memory nor fp64.
 // Tokens behind an element's count are not read; their gradients are zeros.
-template <int F, int HD>
-__global__ void __launch_bounds__(512)
+template <int F, int HD, int MAX_THREADS>
+__global__ void __launch_bounds__(MAX_THREADS + 32, CTAS_PER_SM * 256 / MAX_THREADS)
     qknorm_mrope_bwd_kernel(const uint16_t* __restrict__ qkv, const uint16_t* dqk, int64_t ld_dqk, uint16_t* dx,
                             int64_t ld_dx, float* __restrict__ part, int64_t tokens, int seq, int n_heads, RopeArgs ra,
-                            const uint16_t* __restrict__ g_q, const uint16_t* __restrict__ g_k, float eps) {
+                            const uint16_t* __restrict__ g_q, const uint16_t* __restrict__ g_k, float eps, int stages,
+                            const KernelGuard guard) {
+  const bool is_k = blockIdx.y != 0;
   constexpr int half = HD / 2;
   constexpr int GROUP = HD / 16;  // threads per head
-  __shared__ float s_cos[2][half], s_sin[2][half];
-  __shared__ int s_live[2];
-  extern __shared__ float s_red[];  // [warps][2 HD]
-  pdl_wait_then_release();
+  __shared__ __align__(16) float s_cos[MAX_STAGES][half], s_sin[MAX_STAGES][half];
+  __shared__ uint64_t full[MAX_STAGES], empty[MAX_STAGES];
+  __shared__ uint32_t abort_flag;
+  extern __shared__ __align__(16) uint8_t ring[];  // [stages][raw | gradient]; at the end [warps][HD] sums
   const int per_token = n_heads * GROUP;
+  const int warps = (blockDim.x >> 5) - 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int d = n_heads * HD;
+  const uint32_t row_bytes = 2u * d;
+  const int col = is_k ? d : 0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], warps);
+    }
+    abort_flag = 0u;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_wait_then_release();
+
+  if (warp == warps) {
+    int u = 0;
+    TokenWalk w(seq);
+    for (int64_t bs = blockIdx.x; bs < tokens; bs += gridDim.x, w.step(seq)) {
+      const int b = w.b, s = w.s;
+      if (s >= rope_count(ra, b)) continue;
+      int pt, ph, pw;
+      rope_position(ra, b, s, pt, ph, pw);
+      const int st = u % stages;
+      if (!mbar_wait(&empty[st], (static_cast<uint32_t>(u / stages) & 1u) ^ 1u, guard, &abort_flag,
+                     where_code(ERR_TIMEOUT_QKBWD, 0, u)))
+        break;
+      if (lane == 0) {
+        // the angles below are part of the phase: its one arrival comes after them
+        asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&full[st])),
+                     "r"(2 * row_bytes)
+                     : "memory");
+        bulk_load(ring + st * 2 * row_bytes, qkv + bs * 3 * d + col, row_bytes, &full[st]);
+        bulk_load(ring + st * 2 * row_bytes + row_bytes, dqk + bs * ld_dqk + col, row_bytes, &full[st]);
+      }
+      for (int i = lane; i < half; i += 32)
+        rope_angle(ra, i, i < ra.sec_t ? pt : (i < ra.sec_t + ra.sec_h ? ph : pw), s_cos[st][i], s_sin[st][i]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[st]);
+      ++u;
+    }
+    // never leave with copies in flight
+    for (int v = u > stages ? u - stages : 0; v < u; ++v)
+      mbar_wait(&full[v % stages], static_cast<uint32_t>(v / stages) & 1u, guard, &abort_flag,
+                where_code(ERR_TIMEOUT_QKBWD, 1, v), true);
+    __syncthreads();
+    __syncthreads();
+    return;
+  }
+
   const bool mine = static_cast<int>(threadIdx.x) < per_token;
   const int t = mine ? static_cast<int>(threadIdx.x) : per_token - 1;
   const int c = t % GROUP, h = t / GROUP;
-  const int d = n_heads * HD;
+  float sum[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) sum[k] = 0.f;
+  const uint16_t* g = is_k ? g_k : g_q;
+  const uint4 gain_a = *reinterpret_cast<const uint4*>(g + 8 * c), gain_b = *reinterpret_cast<const uint4*>(g + half + 8 * c);
 
-  struct Vecs {
-    uint4 v[8];  // raw q (two halves), raw k, gradient of q, gradient of k
-  };
-  auto load = [&](int64_t bs, Vecs& w) {
-    const uint16_t* x = qkv + bs * 3 * d + h * HD + 8 * c;
-    const uint16_t* g = dqk + bs * ld_dqk + h * HD + 8 * c;
-    w.v[0] = *reinterpret_cast<const uint4*>(x);
-    w.v[1] = *reinterpret_cast<const uint4*>(x + half);
-    w.v[2] = *reinterpret_cast<const uint4*>(x + d);
-    w.v[3] = *reinterpret_cast<const uint4*>(x + d + half);
-    w.v[4] = *reinterpret_cast<const uint4*>(g);
-    w.v[5] = *reinterpret_cast<const uint4*>(g + half);
-    w.v[6] = *reinterpret_cast<const uint4*>(g + d);
-    w.v[7] = *reinterpret_cast<const uint4*>(g + d + half);
-  };
-  auto angles = [&](int64_t bs, int buf) {
-    const int b = static_cast<int>(bs / seq), s = static_cast<int>(bs - static_cast<int64_t>(b) * seq);
-    int pt, ph, pw;
-    const int count = rope_position(ra, b, s, pt, ph, pw);
-    if (threadIdx.x == 0) s_live[buf] = s < count;
-    for (int i = threadIdx.x; i < half; i += blockDim.x)
-      rope_angle(ra, i, i < ra.sec_t ? pt : (i < ra.sec_t + ra.sec_h ? ph : pw), s_cos[buf][i], s_sin[buf][i]);
-  };
-  float acc[2][16];
+  // one token: x, dy in shared memory (this thread's first half at 0, second at `half`)
+  auto one = [&](const uint16_t* x, const uint16_t* dy, uint16_t* out, const float* cosv, const float* sinv) {
+    float xa[8], xb[8], za[8], zb[8], ga[8], gb[8];
+    load8<F>(x, 0, xa);
+    load8<F>(x + half, 0, xb);
+    load8<F>(dy, 0, za);
+    load8<F>(dy + half, 0, zb);
+    load8<FMT_BF16>(&gain_a, 0, ga);
+    load8<FMT_BF16>(&gain_b, 0, gb);
+    float ss = 0.f, dot = 0.f;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) acc[0][k] = acc[1][k] = 0.f;
-
-  int64_t bs = blockIdx.x;
-  Vecs cur;
-  if (bs < tokens) {
-    load(bs, cur);
-    angles(bs, 0);
-  }
-  __syncthreads();
-  for (int buf = 0; bs < tokens; bs += gridDim.x, buf ^= 1) {
-    const int64_t next = bs + gridDim.x;
-    Vecs nxt;
-    if (next < tokens) {
-      load(next, nxt);
-      angles(next, buf ^ 1);
-    } else {
-      nxt = cur;
-    }
-    uint16_t* out = dx + bs * ld_dx + h * HD + 8 * c;
-    const bool live = s_live[buf] != 0;
+    for (int k4 = 0; k4 < 8; k4 += 4) {
+      const float4 c4 = *reinterpret_cast<const float4*>(cosv + 8 * c + k4);
+      const float4 s4 = *reinterpret_cast<const float4*>(sinv + 8 * c + k4);
+      const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const uint16_t* g = w == 0 ? g_q : g_k;
-      float ga[8], gb[8], xa[8], xb[8], da[8], db[8];
-      load8<FMT_BF16>(g + 8 * c, 0, ga);
-      load8<FMT_BF16>(g + half + 8 * c, 0, gb);
-      load8<F>(&cur.v[2 * w], 0, xa);
-      load8<F>(&cur.v[2 * w + 1], 0, xb);
-      load8<F>(&cur.v[4 + 2 * w], 0, da);
-      load8<F>(&cur.v[4 + 2 * w + 1], 0, db);
-      float ss = 0.f, dot = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float cs = s_cos[buf][8 * c + k], sn = s_sin[buf][8 * c + k];
-        const float za = da[k] * cs + db[k] * sn, zb = db[k] * cs - da[k] * sn;  // R^T dy
+      for (int q = 0; q < 4; ++q) {
+        const int k = k4 + q;
+        const float a = za[k] * cs[q] + zb[k] * sn[q], b = zb[k] * cs[q] - za[k] * sn[q];  // R^T dy
         ss = fmaf(xa[k], xa[k], fmaf(xb[k], xb[k], ss));
-        dot = fmaf(za * ga[k], xa[k], fmaf(zb * gb[k], xb[k], dot));
-        da[k] = za;
-        db[k] = zb;
-      }
-#pragma unroll
-      for (int o = GROUP / 2; o > 0; o >>= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      }
-      const float r = rsqrtf(ss * (1.f / HD) + eps);
-      const float m = dot * (1.f / HD) * r * r;  // xh mean(du xh) = x m
-      float oa[8], ob[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (live) {
-          acc[w][k] = fmaf(da[k], xa[k] * r, acc[w][k]);
-          acc[w][8 + k] = fmaf(db[k], xb[k] * r, acc[w][8 + k]);
-        }
-        oa[k] = live ? r * fmaf(-m, xa[k], da[k] * ga[k]) : 0.f;
-        ob[k] = live ? r * fmaf(-m, xb[k], db[k] * gb[k]) : 0.f;
-      }
-      if (mine) {
-        store8<F>(out + w * d, 0, oa);
-        store8<F>(out + w * d + half, 0, ob);
+        dot = fmaf(a * ga[k], xa[k], fmaf(b * gb[k], xb[k], dot));
+        za[k] = a;
+        zb[k] = b;
       }
     }
-    cur = nxt;
-    __syncthreads();  // the next token's angles are written, this token's are read
+#pragma unroll
+    for (int o = GROUP / 2; o > 0; o >>= 1) {
+      ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    }
+    const float r = rsqrtf(ss * (1.f / HD) + eps);
+    const float m = dot * (1.f / HD) * r * r;  // xh mean(du xh) = x m
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      sum[k] = fmaf(za[k], xa[k] * r, sum[k]);
+      sum[8 + k] = fmaf(zb[k], xb[k] * r, sum[8 + k]);
+      za[k] = r * fmaf(-m, xa[k], za[k] * ga[k]);
+      zb[k] = r * fmaf(-m, xb[k], zb[k] * gb[k]);
+    }
+    if (mine) {
+      store8<F>(out, 0, za);
+      store8<F>(out + half, 0, zb);
+    }
+  };
+
+  int u = 0;
+  TokenWalk w(seq);
+  for (int64_t bs = blockIdx.x; bs < tokens; bs += gridDim.x, w.step(seq)) {
+    uint16_t* out = dx + bs * ld_dx + col + h * HD + 8 * c;
+    if (w.s >= rope_count(ra, w.b)) {  // the whole CTA agrees
+      if (mine) {
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(out) = z;
+        *reinterpret_cast<uint4*>(out + half) = z;
+      }
+      continue;
+    }
+    const int st = u % stages;
+    if (!mbar_wait(&full[st], static_cast<uint32_t>(u / stages) & 1u, guard, &abort_flag,
+                   where_code(ERR_TIMEOUT_QKBWD, 2, u)))
+      break;
+    const uint16_t* x = reinterpret_cast<const uint16_t*>(ring + st * 2 * row_bytes) + h * HD + 8 * c;
+    one(x, x + d, out, s_cos[st], s_sin[st]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
+    ++u;
   }
+  __syncthreads();  // every warp is done with the ring, and its copies have landed
 
   // sum over the CTA's heads: lanes of one warp that share c, then the warps
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  float* s_red = reinterpret_cast<float*>(ring);
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
+  for (int k = 0; k < 16; ++k) {
+    float v = mine ? sum[k] : 0.f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      float v = mine ? acc[w][k] : 0.f;
-#pragma unroll
-      for (int o = 16; o >= GROUP; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane < GROUP) s_red[warp * 2 * HD + w * HD + (k < 8 ? 0 : half) + 8 * lane + (k & 7)] = v;
-    }
+    for (int o = 16; o >= GROUP; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane < GROUP) s_red[warp * HD + (k < 8 ? 0 : half) + 8 * lane + (k & 7)] = v;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * HD; i += blockDim.x) {
+  for (int i = threadIdx.x; i < HD; i += 32 * warps) {
     float v = 0.f;
-    for (int k = 0; k < warps; ++k) v += s_red[k * 2 * HD + i];
-    part[blockIdx.x * static_cast<int64_t>(2 * HD) + i] = v;
+    for (int k = 0; k < warps; ++k) v += s_red[k * HD + i];
+    part[blockIdx.x * static_cast<int64_t>(2 * HD) + (is_k ? HD : 0) + i] = v;
   }
 }
 
 // ------------------------------------------------------------------ RMSNorm rows
 
 // r = (mean x^2 + eps)^(-1/2): dg_i = sum over rows of dy_i x_i r, and
-// dx_i = r (dy_i g_i - x_i r^2 mean(dy g x)) + dres_i.
-// One row per CTA at a time, both of its sums in one reduction; V vectors of 8 per thread, whose
-// gain, gain sums and row stay in registers; the next row is loaded before the reduction.
+// dx_i = r (dy_i g_i - x_i r^2 mean(dy g x)) + dres_i.  Both sums of a row come from one reduction; the
+// gain and its gradient's sums stay in registers.
 template <int F>
-struct Raw8 {
-  uint4 v[F == FMT_F32 ? 2 : 1];
-};
-template <int F>
-__device__ __forceinline__ Raw8<F> fetch8(const void* p, int64_t i8) {
-  Raw8<F> r;
-  constexpr int N = F == FMT_F32 ? 2 : 1;
-#pragma unroll
-  for (int k = 0; k < N; ++k) r.v[k] = reinterpret_cast<const uint4*>(p)[N * i8 + k];
-  return r;
+constexpr int bytes_of() {
+  return F == FMT_F32 ? 4 : 2;
 }
 
+// Rows of up to 512 columns: a warp per row, V vectors of 8 per lane; the next row is loaded before the
+// current one's arithmetic.
 template <int V, int XF, int DF, int OF>
-__global__ void __launch_bounds__(512)
-    rmsnorm_bwd_kernel(const void* __restrict__ x, const uint16_t* __restrict__ g, const void* __restrict__ dy,
-                       const void* dres, void* dx, float* __restrict__ part, int64_t rows, int64_t cols, float eps) {
-  __shared__ float2 red[2][16];
+__global__ void __launch_bounds__(256)
+    rmsnorm_bwd_warp_kernel(const void* __restrict__ x, const uint16_t* __restrict__ g, const void* __restrict__ dy,
+                            const void* dres, void* dx, float* __restrict__ part, int64_t rows, int64_t cols,
+                            float eps) {
+  __shared__ __align__(16) float s_acc[8][V * 256];
   pdl_wait_then_release();
-  const int nv = static_cast<int>(cols / 8);
-  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nv = static_cast<int>(cols / 8), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float inv = 1.f / static_cast<float>(cols);
+  const int64_t step = 8ll * gridDim.x;
+  float gv[V][8], acc[V][8], xn[V][8], yn[V][8];
+  auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int i = lane + 32 * j;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) xn[j][k] = yn[j][k] = 0.f;
+      if (i < nv && row < rows) {
+        load8<XF>(x, row * nv + i, xn[j]);
+        load8<DF>(dy, row * nv + i, yn[j]);
+      }
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) gv[j][k] = acc[j][k] = 0.f;
+    if (lane + 32 * j < nv) load8<FMT_BF16>(g, lane + 32 * j, gv[j]);
+  }
+  fetch(blockIdx.x * 8ll + warp);
+  for (int64_t row = blockIdx.x * 8ll + warp; row < rows; row += step) {
+    float xv[V][8], yv[V][8], e[V][8];
+    float ss = 0.f, dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        xv[j][k] = xn[j][k];
+        yv[j][k] = yn[j][k];
+        e[j][k] = 0.f;
+        ss = fmaf(xv[j][k], xv[j][k], ss);
+        dot = fmaf(yv[j][k] * gv[j][k], xv[j][k], dot);
+      }
+      if (dres != nullptr && lane + 32 * j < nv) load8<OF>(dres, row * nv + lane + 32 * j, e[j]);
+    }
+    fetch(row + step);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    }
+    const float r = rsqrtf(ss * inv + eps);
+    const float m = dot * inv * r * r;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        acc[j][k] = fmaf(yv[j][k], xv[j][k] * r, acc[j][k]);
+        e[j][k] = fmaf(r, fmaf(-m, xv[j][k], yv[j][k] * gv[j][k]), e[j][k]);
+      }
+      if (lane + 32 * j < nv) store8<OF>(dx, row * nv + lane + 32 * j, e[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) store8<FMT_F32>(s_acc[warp], lane + 32 * j, acc[j]);
+  __syncthreads();
+  for (int i = threadIdx.x; i < cols; i += 256) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += s_acc[w][i];
+    part[blockIdx.x * cols + i] = v;
+  }
+}
+
+// Longer rows: a CTA per row at a time, V vectors of 8 per thread.  HBM-bound: x, dy and dres come
+// through a ring of bulk copies that keeps up to 200 KB in flight per SM (from registers, with one row
+// fetched ahead, 4608 x 4096 took 56 us against 47).  A stage is free for its next row when the CTA has
+// met in the following row's reduction.
+template <int V, int XF, int DF, int OF>
+__global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
+    rmsnorm_bwd_kernel(const void* __restrict__ x, const uint16_t* __restrict__ g, const void* __restrict__ dy,
+                       const void* dres, void* dx, float* __restrict__ part, int64_t rows, int64_t cols, float eps,
+                       int stages, const KernelGuard guard) {
+  __shared__ __align__(16) float2 red[2][16];  // entries past the CTA's warps stay zero
+  __shared__ uint64_t full[MAX_STAGES];
+  __shared__ uint32_t abort_flag;
+  extern __shared__ __align__(16) uint8_t ring[];  // [stages][x | dy | dres]
+  const int nv = static_cast<int>(cols / 8);
+  const uint32_t xb = static_cast<uint32_t>(cols) * bytes_of<XF>(), yb = static_cast<uint32_t>(cols) * bytes_of<DF>(),
+                 eb = dres != nullptr ? static_cast<uint32_t>(cols) * bytes_of<OF>() : 0u;
+  const uint32_t stage_bytes = xb + yb + eb;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float inv = 1.f / static_cast<float>(cols);
+  if (threadIdx.x < 32) red[threadIdx.x >> 4][threadIdx.x & 15] = make_float2(0.f, 0.f);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+    abort_flag = 0u;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_wait_then_release();
+  int issued = 0;  // thread 0
+  auto load = [&](int64_t row) {
+    const int st = issued % stages;
+    uint8_t* at = ring + static_cast<size_t>(st) * stage_bytes;
+    mbar_arrive_expect_tx(&full[st], stage_bytes);
+    bulk_load(at, static_cast<const uint8_t*>(x) + row * xb, xb, &full[st]);
+    bulk_load(at + xb, static_cast<const uint8_t*>(dy) + row * yb, yb, &full[st]);
+    if (eb > 0) bulk_load(at + xb + yb, static_cast<const uint8_t*>(dres) + row * eb, eb, &full[st]);
+    ++issued;
+  };
+  if (threadIdx.x == 0) {
+    int64_t row = blockIdx.x;
+    for (int i = 0; i < stages && row < rows; ++i, row += gridDim.x) load(row);
+  }
   float gv[V][8], acc[V][8];
-  Raw8<XF> rx[V];
-  Raw8<DF> ry[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int i = threadIdx.x + j * blockDim.x;
 #pragma unroll
     for (int k = 0; k < 8; ++k) gv[j][k] = acc[j][k] = 0.f;
-    rx[j] = Raw8<XF>{};
-    ry[j] = Raw8<DF>{};
-    if (i < nv) {
-      load8<FMT_BF16>(g, i, gv[j]);
-      if (blockIdx.x < rows) {
-        rx[j] = fetch8<XF>(x, blockIdx.x * static_cast<int64_t>(nv) + i);
-        ry[j] = fetch8<DF>(dy, blockIdx.x * static_cast<int64_t>(nv) + i);
-      }
-    }
+    if (i < nv) load8<FMT_BF16>(g, i, gv[j]);
   }
-  int buf = 0;
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, buf ^= 1) {
-    const int64_t next = row + gridDim.x;
+  int u = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, ++u) {
+    const int st = u % stages, buf = u & 1;
+    if (!mbar_wait(&full[st], static_cast<uint32_t>(u / stages) & 1u, guard, &abort_flag,
+                   where_code(ERR_TIMEOUT_NORMBWD, 0, u)))
+      break;
+    const uint8_t* at = ring + static_cast<size_t>(st) * stage_bytes;
     float xv[V][8], yv[V][8];
     float ss = 0.f, dot = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      load8<XF>(rx[j].v, 0, xv[j]);
-      load8<DF>(ry[j].v, 0, yv[j]);
       const int i = threadIdx.x + j * blockDim.x;
-      if (i < nv && next < rows) {
-        rx[j] = fetch8<XF>(x, next * nv + i);
-        ry[j] = fetch8<DF>(dy, next * nv + i);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) xv[j][k] = yv[j][k] = 0.f;
+      if (i < nv) {
+        load8<XF>(at, i, xv[j]);
+        load8<DF>(at + xb, i, yv[j]);
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -250,10 +403,17 @@ __global__ void __launch_bounds__(512)
     }
     if (lane == 0) red[buf][warp] = make_float2(ss, dot);
     __syncthreads();  // two buffers: the next row's writes cannot meet this row's reads
+    // the CTA is done with the row before this one: its stage takes the row `stages` after it
+    if (threadIdx.x == 0 && u > 0) {
+      const int64_t ahead = row + (stages - 1) * static_cast<int64_t>(gridDim.x);
+      if (ahead < rows) load(ahead);
+    }
     ss = dot = 0.f;
-    for (int w = 0; w < warps; ++w) {
-      ss += red[buf][w].x;
-      dot += red[buf][w].y;
+#pragma unroll
+    for (int w = 0; w < 16; w += 2) {
+      const float4 v = *reinterpret_cast<const float4*>(&red[buf][w]);
+      ss += v.x + v.z;
+      dot += v.y + v.w;
     }
     const float r = rsqrtf(ss * inv + eps);
     const float m = dot * inv * r * r;
@@ -264,7 +424,7 @@ __global__ void __launch_bounds__(512)
       float o[8], e[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) e[k] = 0.f;
-      if (dres != nullptr) load8<OF>(dres, row * nv + i, e);
+      if (eb > 0) load8<OF>(at + xb + yb, i, e);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         acc[j][k] = fmaf(yv[j][k], xv[j][k] * r, acc[j][k]);
@@ -273,6 +433,11 @@ __global__ void __launch_bounds__(512)
       store8<OF>(dx, row * nv + i, o);
     }
   }
+  if (threadIdx.x == 0) {  // never leave with copies in flight
+    for (int v = issued > stages ? issued - stages : 0; v < issued; ++v)
+      mbar_wait(&full[v % stages], static_cast<uint32_t>(v / stages) & 1u, guard, &abort_flag,
+                where_code(ERR_TIMEOUT_NORMBWD, 1, v), true);
+  }
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int i = threadIdx.x + j * blockDim.x;
@@ -280,15 +445,40 @@ __global__ void __launch_bounds__(512)
   }
 }
 
+// CTAs per SM of the long-row kernel, and the grid of both.
+static int norm_ctas_per_sm(int64_t cols) { return cols <= 1024 ? 4 : cols <= 4096 ? 2 : 1; }
+static int norm_grid(int64_t rows, int64_t cols) {
+  if (cols <= 512) {
+    const int64_t want = (rows + 7) / 8;
+    return static_cast<int>(want < 2 * SMS ? want : 2 * SMS);
+  }
+  const int64_t most = static_cast<int64_t>(SMS) * norm_ctas_per_sm(cols);
+  return static_cast<int>(rows < most ? rows : most);
+}
+
 template <int XF, int DF, int OF>
 static cudaError_t launch_norm(const void* x, const uint16_t* g, const void* dy, const void* dres, void* dx,
-                               float* part, int64_t rows, int64_t cols, float eps, int grid, cudaStream_t s) {
+                               float* part, int64_t rows, int64_t cols, float eps, int grid, const KernelGuard& guard,
+                               cudaStream_t s) {
   const int nv = static_cast<int>(cols / 8);
-  if (nv <= 512)
-    return launch_pdl(rmsnorm_bwd_kernel<1, XF, DF, OF>, dim3(grid), dim3((nv + 31) / 32 * 32), 0, s, x, g, dy, dres,
-                      dx, part, rows, cols, eps);
-  return launch_pdl(rmsnorm_bwd_kernel<2, XF, DF, OF>, dim3(grid), dim3(((nv + 1) / 2 + 31) / 32 * 32), 0, s, x, g, dy,
-                    dres, dx, part, rows, cols, eps);
+  if (cols <= 256)
+    return launch_pdl(rmsnorm_bwd_warp_kernel<1, XF, DF, OF>, dim3(grid), dim3(256), 0, s, x, g, dy, dres, dx, part,
+                      rows, cols, eps);
+  if (cols <= 512)
+    return launch_pdl(rmsnorm_bwd_warp_kernel<2, XF, DF, OF>, dim3(grid), dim3(256), 0, s, x, g, dy, dres, dx, part,
+                      rows, cols, eps);
+  const int64_t stage = cols * (bytes_of<XF>() + bytes_of<DF>() + (dres != nullptr ? bytes_of<OF>() : 0));
+  int64_t stages = 212 * 1024 / norm_ctas_per_sm(cols) / stage;
+  stages = stages < 2 ? 2 : stages > MAX_STAGES ? MAX_STAGES : stages;
+  const int smem = static_cast<int>(stages * stage);
+  auto run = [&](auto kern, int threads) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(grid), dim3(threads), smem, s, x, g, dy, dres, dx, part, rows, cols, eps,
+                      static_cast<int>(stages), guard);
+  };
+  if (nv <= 512) return run(rmsnorm_bwd_kernel<1, XF, DF, OF>, (nv + 31) / 32 * 32);
+  return run(rmsnorm_bwd_kernel<2, XF, DF, OF>, ((nv + 1) / 2 + 31) / 32 * 32);
 }
 
 template <int XF, int DF, typename... A>
@@ -305,39 +495,56 @@ static cudaError_t launch_norm_df(int dy_fmt, int dx_fmt, A... a) {
   return launch_norm_of<XF, FMT_F32>(dx_fmt, a...);
 }
 
-static int ctas(int64_t n) { return static_cast<int>(n < MAX_CTAS ? n : MAX_CTAS); }
+// CTAs of the QK-norm gradient for each of q and k.
+static int qk_grid(int64_t tokens, int per_token) {
+  const int64_t most = (per_token <= 256 ? CTAS_PER_SM : CTAS_PER_SM / 2) * SMS / 2;
+  return static_cast<int>(tokens < most ? tokens : most);
+}
 
 }  // namespace tew
 
-size_t qknorm_mrope_bwd_workspace(int64_t tokens, int head_dim) {
-  return static_cast<size_t>(tew::ctas(tokens)) * 2 * head_dim * 4;
+size_t qknorm_mrope_bwd_workspace(int64_t tokens, int n_heads, int head_dim) {
+  return static_cast<size_t>(tew::qk_grid(tokens, n_heads * (head_dim / 16))) * 2 * head_dim * 4;
 }
 
 cudaError_t launch_qknorm_mrope_bwd(const void* qkv, Rows dqk, Rows dx, float* dg_q, float* dg_k, int fmt, int batch,
                                     int seq, int n_heads, int head_dim, int n_text, int grid_w, int n_img, int t_img,
                                     const int32_t* pos, const int32_t* text_lens, const int32_t sections[3],
                                     float theta, const uint16_t* g_q, const uint16_t* g_k, float eps, void* workspace,
-                                    cudaStream_t s) {
+                                    const KernelGuard& guard, cudaStream_t s) {
   const int64_t tokens = static_cast<int64_t>(batch) * seq;
   const int per_token = n_heads * (head_dim / 16);
   if (per_token > 512) return cudaErrorInvalidValue;  // the kernel's launch bound
   const RopeArgs ra = rope_args(n_text, grid_w, n_img, t_img, pos, text_lens, nullptr, sections, theta, head_dim);
-  const int threads = (per_token + 31) / 32 * 32;
-  const int grid = tew::ctas(tokens);
+  const int warps = (per_token + 31) / 32;
+  const int grid = tew::qk_grid(tokens, per_token);
+  // a stage holds the raw rows and their gradients; an SM's CTAs share about 190 KB
+  const int stage = 4 * n_heads * head_dim;
+  int stages = 190 * 1024 / (per_token <= 256 ? tew::CTAS_PER_SM : tew::CTAS_PER_SM / 2) / stage;
+  stages = stages < 2 ? 2 : stages > tew::MAX_STAGES ? tew::MAX_STAGES : stages;
+  const int sums = warps * head_dim * 4;
+  const int smem = stages * stage > sums ? stages * stage : sums;
   float* part = static_cast<float*>(workspace);
   auto run = [&](auto kern) {
-    return launch_pdl(kern, dim3(grid), dim3(threads), static_cast<size_t>(threads / 32) * 2 * head_dim * 4, s,
-                      static_cast<const uint16_t*>(qkv), static_cast<const uint16_t*>(dqk.p), dqk.ld,
-                      static_cast<uint16_t*>(const_cast<void*>(dx.p)), dx.ld, part, tokens, seq, n_heads, ra, g_q, g_k,
-                      eps);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(grid, 2), dim3(32 * (warps + 1)), smem, s, static_cast<const uint16_t*>(qkv),
+                      static_cast<const uint16_t*>(dqk.p), dqk.ld, static_cast<uint16_t*>(const_cast<void*>(dx.p)),
+                      dx.ld, part, tokens, seq, n_heads, ra, g_q, g_k, eps, stages, guard);
+  };
+  auto of = [&](auto hd) {
+    constexpr int HD = decltype(hd)::value;
+    if (per_token <= 256)
+      return fmt == FMT_F16 ? run(tew::qknorm_mrope_bwd_kernel<FMT_F16, HD, 256>)
+                            : run(tew::qknorm_mrope_bwd_kernel<FMT_BF16, HD, 256>);
+    return fmt == FMT_F16 ? run(tew::qknorm_mrope_bwd_kernel<FMT_F16, HD, 512>)
+                          : run(tew::qknorm_mrope_bwd_kernel<FMT_BF16, HD, 512>);
   };
   cudaError_t e;
   if (head_dim == 128)
-    e = fmt == FMT_F16 ? run(tew::qknorm_mrope_bwd_kernel<FMT_F16, 128>)
-                       : run(tew::qknorm_mrope_bwd_kernel<FMT_BF16, 128>);
+    e = of(std::integral_constant<int, 128>());
   else if (head_dim == 64)
-    e = fmt == FMT_F16 ? run(tew::qknorm_mrope_bwd_kernel<FMT_F16, 64>)
-                       : run(tew::qknorm_mrope_bwd_kernel<FMT_BF16, 64>);
+    e = of(std::integral_constant<int, 64>());
   else
     return cudaErrorInvalidValue;
   if (e != cudaSuccess) return e;
@@ -345,19 +552,19 @@ cudaError_t launch_qknorm_mrope_bwd(const void* qkv, Rows dqk, Rows dx, float* d
 }
 
 size_t rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
-  return static_cast<size_t>(tew::ctas(rows)) * static_cast<size_t>(cols) * 4;
+  return static_cast<size_t>(tew::norm_grid(rows, cols)) * static_cast<size_t>(cols) * 4;
 }
 
 cudaError_t launch_rmsnorm_bwd(const void* x, int x_fmt, const uint16_t* g, const void* dy, int dy_fmt,
                                const void* dres, void* dx, int dx_fmt, float* dg, int64_t rows, int64_t cols,
-                               float eps, void* workspace, cudaStream_t s) {
-  const int grid = tew::ctas(rows);
+                               float eps, void* workspace, const KernelGuard& guard, cudaStream_t s) {
+  const int grid = tew::norm_grid(rows, cols);
   float* part = static_cast<float*>(workspace);
   cudaError_t e;
   if (x_fmt == FMT_BF16)
-    e = tew::launch_norm_df<FMT_BF16>(dy_fmt, dx_fmt, x, g, dy, dres, dx, part, rows, cols, eps, grid, s);
+    e = tew::launch_norm_df<FMT_BF16>(dy_fmt, dx_fmt, x, g, dy, dres, dx, part, rows, cols, eps, grid, guard, s);
   else
-    e = tew::launch_norm_df<FMT_F32>(dy_fmt, dx_fmt, x, g, dy, dres, dx, part, rows, cols, eps, grid, s);
+    e = tew::launch_norm_df<FMT_F32>(dy_fmt, dx_fmt, x, g, dy, dres, dx, part, rows, cols, eps, grid, guard, s);
   if (e != cudaSuccess) return e;
   return tew::sum_rows(part, grid, cols, dg, dg, cols, s);
 }
