@@ -38,8 +38,14 @@ constexpr float P_SHIFT = 15.f;  // f16: P is held as 2^15 P
 // The shape of one pass: blocks of R rows of the streamed axis, COLS of them per elementwise thread (a
 // warp works on a 32 x COLS piece), SLOTS blocks of operands in flight.
 // OUT columns of an accumulator are staged per warp for the store; VECS slots of row vectors.
+// dkv's blocks are the largest whose S^T, dP^T, P^T and dS^T (3 R columns) fit TMEM beside dV and dK.
+template <int HD>
 struct DkvShape {
   static constexpr int R = 80, COLS = 16, SLOTS = 3, CUTS_B = 2, OUT = 32, VECS = 5;
+};
+template <>
+struct DkvShape<64> {
+  static constexpr int R = 128, COLS = 32, SLOTS = 3, CUTS_B = 2, OUT = 32, VECS = 5;
 };
 struct DqShape {
   static constexpr int R = 128, COLS = 32, SLOTS = 3, CUTS_B = 1, OUT = 16, VECS = 0;
@@ -165,7 +171,7 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepArgs a) {
     }
   }
   // k: the block in which the tokens end in dq's blocks; q and dO: in dkv's
-  constexpr int RK = DqShape::R, RQ = DkvShape::R;
+  constexpr int RK = DqShape::R, RQ = DkvShape<HD>::R;
   const int k0 = n / RK * RK, q0 = n / RQ * RQ;
   auto reaches = [&](int row0, int rows) { return blk * T < row0 + rows && blk * T + T > row0; };
   const bool tk = has_tail(n, a.seq, RK) && reaches(k0, RK), tq = has_tail(n, a.seq, RQ) && reaches(q0, RQ);
@@ -573,7 +579,7 @@ __device__ __forceinline__ void drain_loads(const Pipe<L, HD>& p, int n_at, int 
 // Own rows: keys; streamed: queries.  The products run with the keys as rows (S^T = K Q^T,
 // dP^T = V dO^T), so that P^T and dS^T come out of the elementwise step in the layout in which the tensor
 // core reads an A operand from TMEM: dV += P^T dO, dK += dS^T Q.
-// Blocks of 80 queries: S^T 80, dP^T 80, P^T 40 and dS^T 40 columns beside dV and dK (128 each) are what
+// Blocks of 80 queries at head dim 128: S^T 80, dP^T 80, P^T 40 and dS^T 40 columns beside dV and dK (128 each) are what
 // TMEM holds with a region of its own for each.  With 128 and P^T over S^T, dS^T over dP^T, S(j+1) waited for
 // dV(j) and dP(j+1) for dK(j): 3420 clocks a block against the products' 2048; with 96 and only
 // dS^T over dP^T 2030 against 1536.
@@ -581,7 +587,7 @@ struct DkvMaps {
   CUtensorMap k, v, q_rows, q_cols, do_rows, do_cols, tq_rows, tq_cols, tdo_rows, tdo_cols, dk, dv;
 };
 template <int HD>
-using DkvLayout = Layout<HD, DkvShape>;
+using DkvLayout = Layout<HD, DkvShape<HD>>;
 
 template <int HD, int F>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREADS, 1)
@@ -602,7 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
   const int ntile = (seq + 2 * T - 1) / (2 * T);
   const int items = batch * n_heads * ntile;
   const uint32_t tmem = begin(p);
-  constexpr int C_DP = R, C_P = 2 * R, C_DS = C_P + R / 2, C_DV = 256, C_DK = 384;
+  constexpr int C_DP = R, C_P = 2 * R, C_DS = C_P + R / 2, C_DV = TMEM_COLS - 2 * HD, C_DK = TMEM_COLS - HD;
   static_assert(C_DS + R / 2 <= C_DV, "TMEM columns");
   pdl_wait_then_release();
 
@@ -1067,28 +1073,29 @@ static cudaError_t launch_hd(Rows q, Rows k, Rows v, const void* out, const void
     ok = ok && map_rows(by_rows, F, r.p, r.ld, n, batch, d, 64, blk / 2);
     if (by_cols != nullptr) ok = ok && map_rows(by_cols, F, r.p, r.ld, n, batch, d, HD / 2, blk);
   };
-  DqMaps mq;
+  DqMaps mq = {};
   tile(&mq.q, q);
   tile(&mq.dout, go);
   cuts(&mq.k_rows, &mq.k_cols, k, seq, LQ::R);
   cuts(&mq.v_rows, nullptr, v, seq, LQ::R);
-  cuts(&mq.tk_rows, &mq.tk_cols, tk, T, LQ::R);
-  DkvMaps mk;
+  if (key_lens != nullptr) cuts(&mq.tk_rows, &mq.tk_cols, tk, T, LQ::R);  // no other call reads a tail
+  DkvMaps mk = {};
   tile(&mk.k, k);
   tile(&mk.v, v);
   cuts(&mk.q_rows, &mk.q_cols, q, seq, LK::R);
   cuts(&mk.do_rows, &mk.do_cols, go, seq, LK::R);
-  cuts(&mk.tq_rows, &mk.tq_cols, tq, T, LK::R);
-  cuts(&mk.tdo_rows, &mk.tdo_cols, tdo, T, LK::R);
+  if (key_lens != nullptr) {
+    cuts(&mk.tq_rows, &mk.tq_cols, tq, T, LK::R);
+    cuts(&mk.tdo_rows, &mk.tdo_cols, tdo, T, LK::R);
+  }
   // boxes of 32 rows x OUT columns, unswizzled
   auto out_map = [&](CUtensorMap* m, Rows r, int cols) { ok = ok && map_rows(m, F, r.p, r.ld, seq, batch, d, cols, 32, true); };
   out_map(&mq.dq, dq, LQ::OUT);
   out_map(&mk.dk, dk, LK::OUT);
   out_map(&mk.dv, dv, LK::OUT);
   if (!ok) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(bwd_dkv_kernel<HD, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, LK::SMEM);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(bwd_dq_kernel<HD, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, LQ::SMEM);
+  cudaError_t e = allow_smem<bwd_dkv_kernel<HD, F>>(LK::SMEM);
+  if (e == cudaSuccess) e = allow_smem<bwd_dq_kernel<HD, F>>(LQ::SMEM);
   if (e != cudaSuccess) return e;
   const PrepArgs pa{static_cast<const uint16_t*>(q.p), static_cast<const uint16_t*>(k.p),
                     static_cast<const uint16_t*>(v.p), static_cast<const uint16_t*>(out),

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace jab {
@@ -69,5 +71,19 @@ size_t rmsnorm_bwd_workspace(int64_t rows, int64_t cols);
 cudaError_t launch_rmsnorm_bwd(const void* x, int x_fmt, const uint16_t* g, const void* dy, int dy_fmt,
                                const void* dres, void* dx, int dx_fmt, float* dg, int64_t rows, int64_t cols,
                                float eps, void* workspace, const KernelGuard& guard, cudaStream_t s);
+
+// Let a kernel have `bytes` of dynamic shared memory, once per device and size: the call costs about a
+// microsecond, which the smallest sizes notice.
+template <auto Kernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<int> set[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && set[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) set[dev].store(bytes, std::memory_order_relaxed);
+  return e;
+}
 
 }  // namespace jab

@@ -471,14 +471,14 @@ static cudaError_t launch_norm(const void* x, const uint16_t* g, const void* dy,
   int64_t stages = 212 * 1024 / norm_ctas_per_sm(cols) / stage;
   stages = stages < 2 ? 2 : stages > MAX_STAGES ? MAX_STAGES : stages;
   const int smem = static_cast<int>(stages * stage);
-  auto run = [&](auto kern, int threads) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto run = [&](auto v) {
+    constexpr int V = decltype(v)::value;
+    const cudaError_t e = allow_smem<rmsnorm_bwd_kernel<V, XF, DF, OF>>(smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(grid), dim3(threads), smem, s, x, g, dy, dres, dx, part, rows, cols, eps,
-                      static_cast<int>(stages), guard);
+    return launch_pdl(rmsnorm_bwd_kernel<V, XF, DF, OF>, dim3(grid), dim3(((nv + V - 1) / V + 31) / 32 * 32), smem, s, x,
+                      g, dy, dres, dx, part, rows, cols, eps, static_cast<int>(stages), guard);
   };
-  if (nv <= 512) return run(rmsnorm_bwd_kernel<1, XF, DF, OF>, (nv + 31) / 32 * 32);
-  return run(rmsnorm_bwd_kernel<2, XF, DF, OF>, ((nv + 1) / 2 + 31) / 32 * 32);
+  return nv <= 512 ? run(std::integral_constant<int, 1>()) : run(std::integral_constant<int, 2>());
 }
 
 template <int XF, int DF, typename... A>
@@ -525,20 +525,21 @@ cudaError_t launch_qknorm_mrope_bwd(const void* qkv, Rows dqk, Rows dx, float* d
   const int sums = warps * head_dim * 4;
   const int smem = stages * stage > sums ? stages * stage : sums;
   float* part = static_cast<float*>(workspace);
-  auto run = [&](auto kern) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto run = [&](auto fm, auto hd, auto most) {
+    constexpr auto kern = tew::qknorm_mrope_bwd_kernel<decltype(fm)::value, decltype(hd)::value, decltype(most)::value>;
+    const cudaError_t e = allow_smem<kern>(smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(grid, 2), dim3(32 * (warps + 1)), smem, s, static_cast<const uint16_t*>(qkv),
                       static_cast<const uint16_t*>(dqk.p), dqk.ld, static_cast<uint16_t*>(const_cast<void*>(dx.p)),
                       dx.ld, part, tokens, seq, n_heads, ra, g_q, g_k, eps, stages, guard);
   };
   auto of = [&](auto hd) {
-    constexpr int HD = decltype(hd)::value;
-    if (per_token <= 256)
-      return fmt == FMT_F16 ? run(tew::qknorm_mrope_bwd_kernel<FMT_F16, HD, 256>)
-                            : run(tew::qknorm_mrope_bwd_kernel<FMT_BF16, HD, 256>);
-    return fmt == FMT_F16 ? run(tew::qknorm_mrope_bwd_kernel<FMT_F16, HD, 512>)
-                          : run(tew::qknorm_mrope_bwd_kernel<FMT_BF16, HD, 512>);
+    const std::integral_constant<int, 256> two_per_sm;
+    const std::integral_constant<int, 512> one_per_sm;
+    const std::integral_constant<int, FMT_F16> f16;
+    const std::integral_constant<int, FMT_BF16> bf16;
+    if (per_token <= 256) return fmt == FMT_F16 ? run(f16, hd, two_per_sm) : run(bf16, hd, two_per_sm);
+    return fmt == FMT_F16 ? run(f16, hd, one_per_sm) : run(bf16, hd, one_per_sm);
   };
   cudaError_t e;
   if (head_dim == 128)
