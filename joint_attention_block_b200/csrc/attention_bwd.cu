@@ -116,21 +116,35 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepArgs a) {
   float* nlse2 = a.nlse2 + (bh * nblk + blk) * T;
   float* ndelta = a.ndelta + (bh * nblk + blk) * T;
   float mdo = 0.f, mv = 0.f;
+  // every load of the CTA is in flight at once; rows that take no part read the element's first row
+  // (a block past the tokens reads none)
+  constexpr int NV = F == FMT_F16 ? PASSES : 1;
+  uint4 ro[PASSES], rg[PASSES], rv[NV];
+  const bool any = blk * T < n;
+  if (any) {
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      const int row = blk * T + p * ROWS + r0;
+      const int64_t at = static_cast<int64_t>(b) * a.seq + (row < n ? row : 0);
+      ro[p] = reinterpret_cast<const uint4*>(a.o + at * d + h * HD)[c];
+      rg[p] = reinterpret_cast<const uint4*>(a.dout + at * d + h * HD)[c];
+      if constexpr (F == FMT_F16) rv[p] = reinterpret_cast<const uint4*>(a.v + at * a.ldv + h * HD)[c];
+    }
+  }
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const int r = p * ROWS + r0;
     const int row = blk * T + r;
     float dot = 0.f, sdo = 0.f, sv = 0.f;
     if (row < n) {
-      const int64_t at = (static_cast<int64_t>(b) * a.seq + row);
       float o[8], g[8];
-      load8<F>(a.o + at * d + h * HD, c, o);
-      load8<F>(a.dout + at * d + h * HD, c, g);
+      load8<F>(&ro[p], 0, o);
+      load8<F>(&rg[p], 0, g);
 #pragma unroll
       for (int k = 0; k < 8; ++k) dot = fmaf(o[k], g[k], dot);
       if constexpr (F == FMT_F16) {
         float v[8];
-        load8<F>(a.v + at * a.ldv + h * HD, c, v);
+        load8<F>(&rv[p], 0, v);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           sdo = fmaf(g[k], g[k], sdo);
@@ -608,6 +622,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
   const int ntile = (seq + 2 * T - 1) / (2 * T);
   const int items = batch * n_heads * ntile;
   const uint32_t tmem = begin(p);
+  if (warp == 0 && lane < static_cast<int>(sizeof(tm) / sizeof(CUtensorMap)))
+    tma_prefetch_desc(reinterpret_cast<const CUtensorMap*>(&tm) + lane);
   constexpr int C_DP = R, C_P = 2 * R, C_DS = C_P + R / 2, C_DV = TMEM_COLS - 2 * HD, C_DK = TMEM_COLS - HD;
   static_assert(C_DS + R / 2 <= C_DV, "TMEM columns");
   pdl_wait_then_release();
@@ -845,6 +861,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DqLayout<HD>::THREAD
   const int ntile = (seq + 2 * T - 1) / (2 * T);
   const int items = batch * n_heads * ntile;
   const uint32_t tmem = begin(p);
+  if (warp == 0 && lane < static_cast<int>(sizeof(tm) / sizeof(CUtensorMap)))
+    tma_prefetch_desc(reinterpret_cast<const CUtensorMap*>(&tm) + lane);
   constexpr int C_DP = R, C_DS = 2 * R, C_DQ = 384;
   static_assert(C_DS + R / 2 <= C_DQ, "TMEM columns");
   // No wait here: this kernel reads nothing that bwd_dkv_kernel writes, and it cannot start before every
@@ -1078,7 +1096,12 @@ static cudaError_t launch_hd(Rows q, Rows k, Rows v, const void* out, const void
   tile(&mq.dout, go);
   cuts(&mq.k_rows, &mq.k_cols, k, seq, LQ::R);
   cuts(&mq.v_rows, nullptr, v, seq, LQ::R);
-  if (key_lens != nullptr) cuts(&mq.tk_rows, &mq.tk_cols, tk, T, LQ::R);  // no other call reads a tail
+  if (key_lens != nullptr) {
+    cuts(&mq.tk_rows, &mq.tk_cols, tk, T, LQ::R);
+  } else {  // no other call reads a tail
+    mq.tk_rows = mq.k_rows;
+    mq.tk_cols = mq.k_cols;
+  }
   DkvMaps mk = {};
   tile(&mk.k, k);
   tile(&mk.v, v);
@@ -1087,6 +1110,11 @@ static cudaError_t launch_hd(Rows q, Rows k, Rows v, const void* out, const void
   if (key_lens != nullptr) {
     cuts(&mk.tq_rows, &mk.tq_cols, tq, T, LK::R);
     cuts(&mk.tdo_rows, &mk.tdo_cols, tdo, T, LK::R);
+  } else {
+    mk.tq_rows = mk.q_rows;
+    mk.tq_cols = mk.q_cols;
+    mk.tdo_rows = mk.do_rows;
+    mk.tdo_cols = mk.do_cols;
   }
   // boxes of 32 rows x OUT columns, unswizzled
   auto out_map = [&](CUtensorMap* m, Rows r, int cols) { ok = ok && map_rows(m, F, r.p, r.ld, seq, batch, d, cols, 32, true); };
