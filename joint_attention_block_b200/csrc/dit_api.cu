@@ -740,6 +740,9 @@ bool rows_ok(const void* p, int64_t ld, int64_t cols) {
   return p != nullptr && aligned16(p) && ld >= cols && ld % 8 == 0 && ld < (1ll << 31);
 }
 
+// What a tensor map can address: strides below 2^40 bytes.
+bool rows_mappable(int seq, int64_t ld) { return static_cast<int64_t>(seq) * ld < (1ll << 39); }
+
 bool ws_ok(const void* p, size_t bytes, size_t need) {
   return p != nullptr && bytes >= need && (reinterpret_cast<uintptr_t>(p) & 255u) == 0;
 }
@@ -814,6 +817,8 @@ int dit_joint_attention_lse(const void* q, int64_t ld_q, const void* k, int64_t 
   if (!rows_ok(q, ld_q, d) || !rows_ok(k, ld_k, d) || !rows_ok(v, ld_v, d) || !rows_ok(out, d, d) || lse == nullptr)
     return DIT_ERR_INVALID_ARG;
   if (out == q || out == k || out == v) return DIT_ERR_INVALID_ARG;
+  for (int64_t ld : {ld_q, ld_k, ld_v})
+    if (!rows_mappable(seq, ld)) return DIT_ERR_UNSUPPORTED;
   if (key_lens != nullptr &&
       !ws_ok(workspace, ws_bytes, dit_joint_attention_lse_workspace_bytes(batch, seq, n_heads, head_dim)))
     return DIT_ERR_WORKSPACE;
@@ -845,6 +850,8 @@ int dit_joint_attention_backward(const void* q, int64_t ld_q, const void* k, int
   for (const void* p : ins)
     if (p == dq || p == dk || p == dv) return DIT_ERR_INVALID_ARG;
   if (dq == dk || dq == dv || dk == dv) return DIT_ERR_INVALID_ARG;
+  for (int64_t ld : {ld_q, ld_k, ld_v, ld_dq, ld_dk, ld_dv})
+    if (!rows_mappable(seq, ld)) return DIT_ERR_UNSUPPORTED;
   if (!ws_ok(workspace, ws_bytes, dit_joint_attention_backward_workspace_bytes(batch, seq, n_heads, head_dim)))
     return DIT_ERR_WORKSPACE;
   KernelGuard g;

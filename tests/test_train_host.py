@@ -33,7 +33,7 @@ def lse_call(lib, q=1024, ldq=128, k=2048, ldk=128, v=4096, ldv=128, out=8192, l
     (dict(heads=0), INVALID), (dict(hd=96), UNSUPPORTED), (dict(out=1024), INVALID), (dict(out=4096), INVALID),
     (dict(lens=512), WORKSPACE), (dict(lens=512, ws=WS, ws_bytes=100), WORKSPACE),
     (dict(lens=512, ws=WS + 16, ws_bytes=1 << 30), WORKSPACE), (dict(batch=70000), INVALID),
-    (dict(seq=1 << 28), INVALID), (dict(ldv=1 << 33), INVALID),
+    (dict(seq=1 << 28), INVALID), (dict(ldv=1 << 33), INVALID), (dict(seq=1 << 20, ldk=1 << 20), UNSUPPORTED),
 ])
 def test_attention_forward_refusals(lib, change, status):
     assert lse_call(lib, **change) == status
@@ -52,6 +52,7 @@ def backward_call(lib, **c):
     (dict(lddv=130), INVALID), (dict(dk=24584), INVALID), (dict(dq=1024), INVALID), (dict(dv=12288), INVALID),
     (dict(dk=20480), INVALID), (dict(hd=32), UNSUPPORTED), (dict(fmt=2), INVALID), (dict(ws=None), WORKSPACE),
     (dict(ws_bytes=255), WORKSPACE), (dict(ws=WS + 128), WORKSPACE), (dict(seq=-1), INVALID),
+    (dict(seq=1 << 20, lddk=1 << 20), UNSUPPORTED),
 ])
 def test_attention_backward_refusals(lib, change, status):
     assert backward_call(lib, **change) == status
