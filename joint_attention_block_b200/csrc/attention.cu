@@ -46,7 +46,6 @@
 // included: a masked logit is replaced, and the value block in which the tokens end comes from a
 // zero-padded copy (tm_vt), since P = 0 times a NaN value would be NaN inside the tensor core.
 #include "common.cuh"
-#include "pipeline.cuh"
 #include "qk8.h"
 #include "train.h"
 
@@ -227,7 +226,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // ---------------- TMA producer: per work item this CTA's rows of Q_A and Q_B (once the
     // previous item's S MMAs have read Q), then its K and V halves of every key block, through
     // the key/value ring that runs on across items
-    const bool one = elect_one();
     int issued = 0;    // key blocks issued, all items
     int q_issued = 0;  // work items whose Q load was issued
     int ui = 0;        // work items started
@@ -239,7 +237,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         ok = false;
         break;
       }
-      if (one) {
+      if (lane == 0) {
         if (leader) mbar_arrive_expect_tx(q_full, 2 * 2 * L::Q_TILE);
         const uint32_t qbar = mapa_shared(smem_u32(q_full), 0);
         for (int t = 0; t < 2; ++t) {
@@ -262,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           ok = false;
           break;
         }
-        if (one) {
+        if (lane == 0) {
           if (leader) {
             mbar_arrive_expect_tx(&k_full[st], 2 * L::K_BYTES);
             mbar_arrive_expect_tx(&v_full[st], 2 * L::V_BYTES);
@@ -302,8 +300,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else if (warp == 1) {
     // ---------------- MMA issuer (leader only)
     if (leader) {
-      const bool one = elect_one();
-      // kind::f16 for 16-bit q, k; kind::f8f6f4 (type code 0: e4m3) for Q8
+        // kind::f16 for 16-bit q, k; kind::f8f6f4 (type code 0: e4m3) for Q8
       constexpr uint32_t idesc_s = idesc_f16kind(2 * BQ, BKV, Q8 ? true : kF16, false, false);
       constexpr uint32_t idesc_o = idesc_f16kind(2 * BQ, HD, kF16, false, true);
       // g: key block index over all work items (the ring slot and the barrier phases); j: the
@@ -352,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                        where_code(ERR_TIMEOUT_ATTN_MMA, rank, gb));
         if (!ok) break;
         tc_fence_after();
-        if (one) {
+        if (lane == 0) {
           issue_s(0, gb);
           issue_s(1, gb);
           if (nb == 1) mma_commit_pair(q_empty, 0x3);  // the item's last S MMAs are issued: Q free after them
@@ -375,7 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                           where_code(ERR_TIMEOUT_ATTN_MMA, 5, g)));
           if (!ok) break;
           tc_fence_after();
-          if (one) {
+          if (lane == 0) {
             issue_pv(0, g, j);
             if (next) issue_s(0, g + 1);  // overwrites P_A only after P V_A has read it (in-order issue)
           }
@@ -386,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                           where_code(ERR_TIMEOUT_ATTN_MMA, 6, g)));
           if (!ok) break;
           tc_fence_after();
-          if (one) {
+          if (lane == 0) {
             issue_pv(1, g, j);
             mma_commit_pair(&kv_empty[st], 0x3);  // K_g and V_g fully consumed by both tiles
             if (next) {
@@ -396,11 +393,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           }
           __syncwarp();
         }
-        if (ok && one) mma_commit_pair(o_full, 0x3);  // this item's O final
+        if (ok && lane == 0) mma_commit_pair(o_full, 0x3);  // this item's O final
         __syncwarp();
         gb += nb;
       }
-      if (one) mma_commit_pair(drain_bar, 0x3);  // all MMAs retired before either CTA frees TMEM
+      if (lane == 0) mma_commit_pair(drain_bar, 0x3);  // all MMAs retired before either CTA frees TMEM
       __syncwarp();
     }
     mbar_wait(drain_bar, 0u, guard, abort_flag, where_code(ERR_TIMEOUT_ATTN_DRAIN, rank, 1), true);
@@ -527,6 +524,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&p_full[t]), 0));
     }
     if (!ok) break;
+    if constexpr (LSE) {  // while the last P V runs; m_used is in log2 units of the scaled logits
+      const Item it = item(pair + ui * pairs);
+      const int row = it.q0 + 2 * BQ * t + r;
+      if (row < seq)
+        lse[(static_cast<size_t>(it.b) * n_heads + it.head) * seq + row] =
+            row < it.live ? (m_used + log2f(l)) * 0.6931471805599453f : 0.f;
+    }
     if (!mbar_wait(o_full, static_cast<uint32_t>(ui) & 1u, guard, abort_flag,
                    where_code(ERR_TIMEOUT_ATTN_SOFTMAX, 4 + rank, t))) {
       ok = false;
@@ -538,12 +542,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const float inv_l = 1.f / l;
       const int row = it.q0 + 2 * BQ * t + r;
       uint16_t* dst = out + (static_cast<size_t>(it.b) * seq + row) * d + it.head * HD;
-      if constexpr (LSE) {
-        // m_used and l are in log2 units of the scaled logits
-        if (row < seq)
-          lse[(static_cast<size_t>(it.b) * n_heads + it.head) * seq + row] =
-              row < it.live ? (m_used + log2f(l)) * 0.6931471805599453f : 0.f;
-      }
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c) {
         uint32_t raw[32];
