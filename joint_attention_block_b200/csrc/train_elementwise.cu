@@ -74,12 +74,12 @@ struct TokenWalk {
 // dx = r (du - xh mean(du xh)).
 // A CTA works on q or on k (blockIdx.y) and walks tokens with the gain's sums in registers (q and k
 // together needed more registers than two CTAs of an SM have); thread layout as in the forward kernel,
-// one thread per head and 8 rotary pairs.  The last warp runs ahead: it copies a token's raw rows and
-// gradients into a ring of shared memory with two bulk copies and computes its angles beside them, so
-// that the other warps wait for neither memory nor fp64.
+// one thread per head and 8 rotary pairs.  The last two warps run ahead: they copy a token's raw rows and
+// gradients into a ring of shared memory with two bulk copies and compute its angles beside them, an
+// angle per lane, so that the other warps wait for neither memory nor fp64.
 // Tokens behind an element's count are not read; their gradients are zeros.
 template <int F, int HD, int MAX_THREADS>
-__global__ void __launch_bounds__(MAX_THREADS + 32, CTAS_PER_SM * 256 / MAX_THREADS)
+__global__ void __launch_bounds__(MAX_THREADS + 64, CTAS_PER_SM * 256 / MAX_THREADS)
     qknorm_mrope_bwd_kernel(const uint16_t* __restrict__ qkv, const uint16_t* dqk, int64_t ld_dqk, uint16_t* dx,
                             int64_t ld_dx, float* __restrict__ part, int64_t tokens, int seq, int n_heads, RopeArgs ra,
                             const uint16_t* __restrict__ g_q, const uint16_t* __restrict__ g_k, float eps, int stages,
@@ -92,13 +92,13 @@ __global__ void __launch_bounds__(MAX_THREADS + 32, CTAS_PER_SM * 256 / MAX_THRE
   __shared__ uint32_t abort_flag;
   extern __shared__ __align__(16) uint8_t ring[];  // [stages][raw | gradient]; at the end [warps][HD] sums
   const int per_token = n_heads * GROUP;
-  const int warps = (blockDim.x >> 5) - 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warps = (blockDim.x >> 5) - 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int d = n_heads * HD;
   const uint32_t row_bytes = 2u * d;
   const int col = is_k ? d : 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], 2);
       mbar_init(&empty[i], warps);
     }
     abort_flag = 0u;
@@ -107,7 +107,8 @@ __global__ void __launch_bounds__(MAX_THREADS + 32, CTAS_PER_SM * 256 / MAX_THRE
   __syncthreads();
   pdl_wait_then_release();
 
-  if (warp == warps) {
+  if (warp >= warps) {
+    const bool first = warp == warps;
     int u = 0;
     TokenWalk w(seq);
     for (int64_t bs = blockIdx.x; bs < tokens; bs += gridDim.x, w.step(seq)) {
@@ -119,24 +120,26 @@ __global__ void __launch_bounds__(MAX_THREADS + 32, CTAS_PER_SM * 256 / MAX_THRE
       if (!mbar_wait(&empty[st], (static_cast<uint32_t>(u / stages) & 1u) ^ 1u, guard, &abort_flag,
                      where_code(ERR_TIMEOUT_QKBWD, 0, u)))
         break;
-      if (lane == 0) {
-        // the angles below are part of the phase: its one arrival comes after them
+      if (first && lane == 0) {
+        // the angles below are part of the phase: its two arrivals come after them
         asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&full[st])),
                      "r"(2 * row_bytes)
                      : "memory");
         bulk_load(ring + st * 2 * row_bytes, qkv + bs * 3 * d + col, row_bytes, &full[st]);
         bulk_load(ring + st * 2 * row_bytes + row_bytes, dqk + bs * ld_dqk + col, row_bytes, &full[st]);
       }
-      for (int i = lane; i < half; i += 32)
+      if (const int i = first ? lane : lane + 32; i < half)
         rope_angle(ra, i, i < ra.sec_t ? pt : (i < ra.sec_t + ra.sec_h ? ph : pw), s_cos[st][i], s_sin[st][i]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[st]);
       ++u;
     }
     // never leave with copies in flight
-    for (int v = u > stages ? u - stages : 0; v < u; ++v)
-      mbar_wait(&full[v % stages], static_cast<uint32_t>(v / stages) & 1u, guard, &abort_flag,
-                where_code(ERR_TIMEOUT_QKBWD, 1, v), true);
+    if (first) {
+      for (int v = u > stages ? u - stages : 0; v < u; ++v)
+        mbar_wait(&full[v % stages], static_cast<uint32_t>(v / stages) & 1u, guard, &abort_flag,
+                  where_code(ERR_TIMEOUT_QKBWD, 1, v), true);
+    }
     __syncthreads();
     __syncthreads();
     return;
@@ -529,7 +532,7 @@ cudaError_t launch_qknorm_mrope_bwd(const void* qkv, Rows dqk, Rows dx, float* d
     constexpr auto kern = tew::qknorm_mrope_bwd_kernel<decltype(fm)::value, decltype(hd)::value, decltype(most)::value>;
     const cudaError_t e = allow_smem<kern>(smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(grid, 2), dim3(32 * (warps + 1)), smem, s, static_cast<const uint16_t*>(qkv),
+    return launch_pdl(kern, dim3(grid, 2), dim3(32 * (warps + 2)), smem, s, static_cast<const uint16_t*>(qkv),
                       static_cast<const uint16_t*>(dqk.p), dqk.ld, static_cast<uint16_t*>(const_cast<void*>(dx.p)),
                       dx.ld, part, tokens, seq, n_heads, ra, g_q, g_k, eps, stages, guard);
   };
