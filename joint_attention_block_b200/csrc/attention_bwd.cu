@@ -99,13 +99,18 @@ struct PrepArgs {
 };
 
 // One CTA per (block of 128 rows, head, element); HD / 8 lanes per row.  HBM-bound: reads O and dO
-// (f16: and V) once.
+// (f16: and V) once.  4608 tokens x 32 heads of 128, L2 cold: bf16 19.5 us (75 MB, 3.9 TB/s), f16
+// 26.4 us (113 MB, 4.3 TB/s), 2-3 % of the whole gradient.  Latency counts in the small calls, so each
+// thread has few rows and loads two of them at a time: 1100 tokens x 16 heads 6.7 us and 80 tokens x 4
+// heads 3.8, against 9.2 and 5.2 with 256 threads; one row at a time 17.8 / 25.0 / 7.7 / 4.4 us; with all
+// rows' loads of 256 threads in flight the registers cost the large f16 call 36 us.
+constexpr int PREP_THREADS = 512;
 template <int HD, int F>
-__global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepArgs a) {
+__global__ void __launch_bounds__(PREP_THREADS) bwd_prep_kernel(const PrepArgs a) {
   constexpr int LANES = HD / 8;
-  constexpr int ROWS = 256 / LANES;
+  constexpr int ROWS = PREP_THREADS / LANES;
   constexpr int PASSES = T / ROWS;
-  __shared__ float2 red[8];
+  __shared__ float2 red[PREP_THREADS / 32];
   pdl_wait_then_release();
   const int blk = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const int nblk = gridDim.x;
@@ -116,56 +121,59 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepArgs a) {
   float* nlse2 = a.nlse2 + (bh * nblk + blk) * T;
   float* ndelta = a.ndelta + (bh * nblk + blk) * T;
   float mdo = 0.f, mv = 0.f;
-  // every load of the CTA is in flight at once; rows that take no part read the element's first row
-  // (a block past the tokens reads none)
-  constexpr int NV = F == FMT_F16 ? PASSES : 1;
-  uint4 ro[PASSES], rg[PASSES], rv[NV];
+  // rows that take no part read the element's first row (a block past the tokens reads none)
+  constexpr int CHUNK = 2;
+  static_assert(PASSES % CHUNK == 0, "whole chunks");
   const bool any = blk * T < n;
-  if (any) {
+#pragma unroll 1
+  for (int p0 = 0; p0 < PASSES; p0 += CHUNK) {
+    uint4 ro[CHUNK], rg[CHUNK], rv[F == FMT_F16 ? CHUNK : 1];
+    if (any) {
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int row = blk * T + p * ROWS + r0;
-      const int64_t at = static_cast<int64_t>(b) * a.seq + (row < n ? row : 0);
-      ro[p] = reinterpret_cast<const uint4*>(a.o + at * d + h * HD)[c];
-      rg[p] = reinterpret_cast<const uint4*>(a.dout + at * d + h * HD)[c];
-      if constexpr (F == FMT_F16) rv[p] = reinterpret_cast<const uint4*>(a.v + at * a.ldv + h * HD)[c];
+      for (int p = 0; p < CHUNK; ++p) {
+        const int row = blk * T + (p0 + p) * ROWS + r0;
+        const int64_t at = static_cast<int64_t>(b) * a.seq + (row < n ? row : 0);
+        ro[p] = reinterpret_cast<const uint4*>(a.o + at * d + h * HD)[c];
+        rg[p] = reinterpret_cast<const uint4*>(a.dout + at * d + h * HD)[c];
+        if constexpr (F == FMT_F16) rv[p] = reinterpret_cast<const uint4*>(a.v + at * a.ldv + h * HD)[c];
+      }
     }
-  }
 #pragma unroll
-  for (int p = 0; p < PASSES; ++p) {
-    const int r = p * ROWS + r0;
-    const int row = blk * T + r;
-    float dot = 0.f, sdo = 0.f, sv = 0.f;
-    if (row < n) {
-      float o[8], g[8];
-      load8<F>(&ro[p], 0, o);
-      load8<F>(&rg[p], 0, g);
+    for (int p = 0; p < CHUNK; ++p) {
+      const int r = (p0 + p) * ROWS + r0;
+      const int row = blk * T + r;
+      float dot = 0.f, sdo = 0.f, sv = 0.f;
+      if (row < n) {
+        float o[8], g[8];
+        load8<F>(&ro[p], 0, o);
+        load8<F>(&rg[p], 0, g);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) dot = fmaf(o[k], g[k], dot);
-      if constexpr (F == FMT_F16) {
-        float v[8];
-        load8<F>(&rv[p], 0, v);
+        for (int k = 0; k < 8; ++k) dot = fmaf(o[k], g[k], dot);
+        if constexpr (F == FMT_F16) {
+          float v[8];
+          load8<F>(&rv[p], 0, v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          sdo = fmaf(g[k], g[k], sdo);
-          sv = fmaf(v[k], v[k], sv);
+          for (int k = 0; k < 8; ++k) {
+            sdo = fmaf(g[k], g[k], sdo);
+            sv = fmaf(v[k], v[k], sv);
+          }
         }
       }
-    }
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) {
-      dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if constexpr (F == FMT_F16) {
-        sdo += __shfl_xor_sync(0xffffffffu, sdo, o);
-        sv += __shfl_xor_sync(0xffffffffu, sv, o);
+      for (int o = LANES / 2; o > 0; o >>= 1) {
+        dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if constexpr (F == FMT_F16) {
+          sdo += __shfl_xor_sync(0xffffffffu, sdo, o);
+          sv += __shfl_xor_sync(0xffffffffu, sv, o);
+        }
       }
-    }
-    mdo = fmaxf(mdo, sdo);
-    mv = fmaxf(mv, sv);
-    if (c == 0) {
-      // rows that take no part: exp2(s - inf) = 0
-      ndelta[r] = -dot;
-      nlse2[r] = row < n ? (F == FMT_F16 ? P_SHIFT : 0.f) - a.lse[bh * a.seq + row] * LOG2E : -INFINITY;
+      mdo = fmaxf(mdo, sdo);
+      mv = fmaxf(mv, sv);
+      if (c == 0) {
+        // rows that take no part: exp2(s - inf) = 0
+        ndelta[r] = -dot;
+        nlse2[r] = row < n ? (F == FMT_F16 ? P_SHIFT : 0.f) - a.lse[bh * a.seq + row] * LOG2E : -INFINITY;
+      }
     }
   }
   if constexpr (F == FMT_F16) {
@@ -177,7 +185,7 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepArgs a) {
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(mdo, mv);
     __syncthreads();
     if (threadIdx.x == 0) {
-      for (int w = 1; w < 8; ++w) {
+      for (int w = 1; w < PREP_THREADS / 32; ++w) {
         mdo = fmaxf(mdo, red[w].x);
         mv = fmaxf(mv, red[w].y);
       }
@@ -1129,7 +1137,7 @@ static cudaError_t launch_hd(Rows q, Rows k, Rows v, const void* out, const void
                     static_cast<const uint16_t*>(v.p), static_cast<const uint16_t*>(out),
                     static_cast<const uint16_t*>(dout), q.ld, k.ld, v.ld, lse, key_lens, w.nlse2, w.ndelta, w.norms2,
                     w.tails, batch, seq, n_heads};
-  e = launch_pdl(bwd_prep_kernel<HD, F>, dim3(nblk, n_heads, batch), dim3(256), 0, s, pa);
+  e = launch_pdl(bwd_prep_kernel<HD, F>, dim3(nblk, n_heads, batch), dim3(PREP_THREADS), 0, s, pa);
   if (e != cudaSuccess) return e;
   int sms = 0, dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
