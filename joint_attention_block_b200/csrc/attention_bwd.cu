@@ -440,17 +440,76 @@ struct Item {
   int b, head, tt, n, nb;  // n: tokens of the element; nb: blocks of the other axis (0: no row takes part)
   int64_t bh;
 };
+// The items in the order in which the pairs are dealt them, pair p taking p, p + pairs, ...  In a padded
+// batch the tiles that hold tokens come first, element by element, then the others, which are only zeroed:
+// with every element's tiles together the pairs' shares of the products came out uneven (1535, 1100, 1324
+// and 1023 tokens padded to 1535, 16 heads of 64: 148 us, now 139; 128 channels: 187, now 173).  Elements
+// of one tile stay together: they are uneven by a few blocks at most, and finding the place costs more
+// (512 elements of 80 or 10 tokens x 4 heads of 64: 191 us, in the other order 210).
+// Items are asked for in rising order, by whole warps: lane l holds the tiles of element chunk + l, summed
+// over the lanes up to it.
 template <int R>
-__device__ __forceinline__ Item item_of(int i, int ntile, int n_heads, int seq, const int32_t* key_lens) {
-  Item it;
-  it.tt = i % ntile;
-  it.bh = i / ntile;
-  it.head = static_cast<int>(it.bh % n_heads);
-  it.b = static_cast<int>(it.bh / n_heads);
-  it.n = tokens_of(key_lens, it.b, seq);
-  it.nb = it.tt * 2 * T < it.n ? (it.n + R - 1) / R : 0;
-  return it;
-}
+struct Items {
+  int batch, ntile, n_heads, seq;
+  const int32_t* key_lens;
+  int total, live;  // items; the first `live` hold tokens (elements of one tile: unless they have none)
+  int chunk = 0, base = 0, upto = 0;
+  bool past = false;
+
+  __device__ Items(int batch, int n_heads, int seq, const int32_t* key_lens)
+      : batch(batch), ntile((seq + 2 * T - 1) / (2 * T)), n_heads(n_heads), seq(seq), key_lens(key_lens) {
+    total = live = batch * n_heads * ntile;
+    if (key_lens == nullptr || ntile == 1) return;
+    int tiles = 0;
+    for (int e = static_cast<int>(lane_id()); e < batch; e += 32) tiles += tiles_of(e);
+    live = n_heads * __reduce_add_sync(0xffffffffu, tiles);
+    sum_chunk();
+  }
+  __device__ __forceinline__ int tiles_of(int e) const { return (tokens_of(key_lens, e, seq) + 2 * T - 1) / (2 * T); }
+  __device__ __forceinline__ void sum_chunk() {
+    const int lane = static_cast<int>(lane_id()), e = chunk + lane;
+    upto = e >= batch ? 0 : past ? ntile - tiles_of(e) : tiles_of(e);
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+  }
+  __device__ __forceinline__ Item at(int i) {
+    Item it;
+    if (key_lens == nullptr || ntile == 1) {
+      it.tt = i % ntile;
+      const int bh = i / ntile;
+      it.head = bh % n_heads;
+      it.b = bh / n_heads;
+      it.n = tokens_of(key_lens, it.b, seq);
+    } else {
+      if (i >= live && !past) {
+        past = true;
+        chunk = 0;
+        base = live;
+        sum_chunk();
+      }
+      while (chunk + 32 < batch) {
+        const int all = n_heads * __shfl_sync(0xffffffffu, upto, 31);
+        if (i - base < all) break;
+        base += all;
+        chunk += 32;
+        sum_chunk();
+      }
+      const int k = min(__popc(__ballot_sync(0xffffffffu, i - base >= n_heads * upto)), 31);
+      const int before = __shfl_sync(0xffffffffu, upto, max(k - 1, 0)) * (k > 0);
+      const int w = max(__shfl_sync(0xffffffffu, upto, k) - before, 1), r = i - base - n_heads * before;
+      it.b = chunk + k;
+      it.n = tokens_of(key_lens, it.b, seq);
+      it.head = r / w;
+      it.tt = r % w + (past ? tiles_of(it.b) : 0);
+    }
+    it.bh = static_cast<int64_t>(it.b) * n_heads + it.head;
+    it.nb = past ? 0 : (it.n + R - 1) / R;  // 0 too for an element of no tokens
+    return it;
+  }
+};
 
 // What both passes share: two CTAs on two SMs (a cluster) own 256 rows of one head, 128 each, and walk
 // the other axis in blocks; the pair MMA (cta_group::2, M = 256) lets each CTA hold half of every block.
@@ -537,14 +596,13 @@ __device__ __forceinline__ void finish(uint32_t tmem) {
 // Warp 1 of the leader: S and dP of every block.
 template <class L, int HD, int F>
 __device__ __forceinline__ void issue_s_dp(const Pipe<L, HD>& p, uint32_t t_s, uint32_t t_dp, int pair, int pairs,
-                                           int items, int ntile, int n_heads, int seq, const int32_t* key_lens,
-                                           const KernelGuard& guard) {
+                                           Items<L::R>& items, const KernelGuard& guard) {
   const bool one = elect_one();
   auto where = [&](int k, int i) { return where_code(ERR_TIMEOUT_ABWD_MMA, k, i); };
   bool ok = true;
   int u = 0, ui = 0;
-  for (int i = pair; i < items && ok; i += pairs) {
-    const int nb = item_of<L::R>(i, ntile, n_heads, seq, key_lens).nb;
+  for (int i = pair; i < items.live && ok; i += pairs) {
+    const int nb = items.at(i).nb;
     if (nb == 0) continue;
     ok = p.at.wait_full(ui, guard, p.abort_flag, where(0, u));
     for (int j = 0; j < nb && ok; ++j, ++u) {
@@ -627,8 +685,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int nblk = blocks_of(seq) + 1;
-  const int ntile = (seq + 2 * T - 1) / (2 * T);
-  const int items = batch * n_heads * ntile;
+  // before the wait: the lengths were in memory before any CTA of bwd_prep_kernel let this kernel start
+  Items<R> items(batch, n_heads, seq, key_lens);
   const uint32_t tmem = begin(p);
   if (warp == 0 && lane < static_cast<int>(sizeof(tm) / sizeof(CUtensorMap)))
     tma_prefetch_desc(reinterpret_cast<const CUtensorMap*>(&tm) + lane);
@@ -641,8 +699,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
     int u = 0, ui = 0, n_b = 0, n_bt = 0, n_at = 0;
     bool ok = true;
     auto where = [&](int i) { return where_code(ERR_TIMEOUT_ABWD_PRODUCER, rank, i); };
-    for (int i = pair; i < items && ok; i += pairs) {
-      const Item it = item_of<R>(i, ntile, n_heads, seq, key_lens);
+    for (int i = pair; i < items.live && ok; i += pairs) {
+      const Item it = items.at(i);
       if (it.nb == 0) continue;
       const bool tail = has_tail(it.n, seq, R);
       const int x = it.head * HD, row0 = it.tt * 2 * T + rank * T;
@@ -693,7 +751,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
     drain_loads(p, n_at, n_bt, u, n_b, u, rank, guard);
   } else if (warp == 1) {
     if (leader)
-      issue_s_dp<L, HD, F>(p, tmem, tmem + C_DP, pair, pairs, items, ntile, n_heads, seq, key_lens, guard);
+      issue_s_dp<L, HD, F>(p, tmem, tmem + C_DP, pair, pairs, items, guard);
     mbar_wait(p.drain_bar, 0u, guard, p.abort_flag, where_code(ERR_TIMEOUT_ABWD_DRAIN, rank, 1), true);
   } else if (warp == 2) {
     if (leader) {
@@ -701,8 +759,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
       auto where = [&](int k, int i) { return where_code(ERR_TIMEOUT_ABWD_MMA, k, i); };
       bool ok = true;
       int u = 0, ui = 0;
-      for (int i = pair; i < items && ok; i += pairs) {
-        const int nb = item_of<R>(i, ntile, n_heads, seq, key_lens).nb;
+      for (int i = pair; i < items.live && ok; i += pairs) {
+        const int nb = items.at(i).nb;
         if (nb == 0) continue;
         // the first dV of an item overwrites accumulators that both CTAs must have read
         ok = ui == 0 || mbar_wait(p.acc_empty, static_cast<uint32_t>(ui - 1) & 1u, guard, p.abort_flag, where(5, u));
@@ -752,15 +810,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
     };
     uint8_t* stage = smem + L::OFF_OUT + (warp - L::FIRST_EW) * 32 * L::OUT * 2;
     auto shift_of = [&](int i) {
-      if (F != FMT_F16 || i >= items) return 0.f;
-      const Item it = item_of<R>(i, ntile, n_heads, seq, key_lens);
+      if (F != FMT_F16 || i >= items.live) return 0.f;
+      const Item it = items.at(i);
       return ds_shift<F>(norms2 + it.bh * nblk, blocks_of(it.n));
     };
     bool ok = true;
     int u = 0, ui = 0;
     float shift = shift_of(pair);
-    for (int i = pair; i < items && ok; i += pairs) {
-      const Item it = item_of<R>(i, ntile, n_heads, seq, key_lens);
+    for (int i = pair; i < items.total && ok; i += pairs) {
+      const Item it = items.at(i);
       const int row0 = it.tt * 2 * T + rank * T;
       if (it.nb == 0) {
         shift = shift_of(i + pairs);
@@ -866,8 +924,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DqLayout<HD>::THREAD
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int nblk = blocks_of(seq) + 1;
-  const int ntile = (seq + 2 * T - 1) / (2 * T);
-  const int items = batch * n_heads * ntile;
+  Items<R> items(batch, n_heads, seq, key_lens);
   const uint32_t tmem = begin(p);
   if (warp == 0 && lane < static_cast<int>(sizeof(tm) / sizeof(CUtensorMap)))
     tma_prefetch_desc(reinterpret_cast<const CUtensorMap*>(&tm) + lane);
@@ -883,8 +940,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DqLayout<HD>::THREAD
     int u = 0, ui = 0, n_b = 0, n_at = 0, n_bt = 0;
     bool ok = true;
     auto where = [&](int i) { return where_code(ERR_TIMEOUT_ABWD_PRODUCER, 2 + rank, i); };
-    for (int i = pair; i < items && ok; i += pairs) {
-      const Item it = item_of<R>(i, ntile, n_heads, seq, key_lens);
+    for (int i = pair; i < items.live && ok; i += pairs) {
+      const Item it = items.at(i);
       if (it.nb == 0) continue;
       const bool tail = has_tail(it.n, seq, R);
       const int x = it.head * HD, row0 = it.tt * 2 * T + rank * T;
@@ -926,7 +983,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DqLayout<HD>::THREAD
     drain_loads(p, n_at, n_bt, u, n_b, 0, rank, guard);
   } else if (warp == 1) {
     if (leader)
-      issue_s_dp<L, HD, F>(p, tmem, tmem + C_DP, pair, pairs, items, ntile, n_heads, seq, key_lens, guard);
+      issue_s_dp<L, HD, F>(p, tmem, tmem + C_DP, pair, pairs, items, guard);
     mbar_wait(p.drain_bar, 0u, guard, p.abort_flag, where_code(ERR_TIMEOUT_ABWD_DRAIN, rank, 3), true);
   } else if (warp == 2) {
     if (leader) {
@@ -934,8 +991,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DqLayout<HD>::THREAD
       auto where = [&](int k, int i) { return where_code(ERR_TIMEOUT_ABWD_MMA, k, i); };
       bool ok = true;
       int u = 0, ui = 0;
-      for (int i = pair; i < items && ok; i += pairs) {
-        const int nb = item_of<R>(i, ntile, n_heads, seq, key_lens).nb;
+      for (int i = pair; i < items.live && ok; i += pairs) {
+        const int nb = items.at(i).nb;
         if (nb == 0) continue;
         // the first dQ of an item overwrites an accumulator that both CTAs must have read
         ok = ui == 0 || mbar_wait(p.acc_empty, static_cast<uint32_t>(ui - 1) & 1u, guard, p.abort_flag, where(9, u));
@@ -980,8 +1037,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DqLayout<HD>::THREAD
     // the padded row vectors reach past the pair's 256 rows
     auto state_of = [&](int i) {
       RowState s{0.f, 0.f, 0.f};
-      if (i >= items) return s;
-      const Item it = item_of<R>(i, ntile, n_heads, seq, key_lens);
+      if (i >= items.live) return s;
+      const Item it = items.at(i);
       const int64_t at = it.bh * nblk * T + it.tt * 2 * T + rank * T + r;
       s.nl = nlse2[at];
       s.nd = ndelta[at];
@@ -991,8 +1048,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DqLayout<HD>::THREAD
     bool ok = true;
     int u = 0, ui = 0;
     RowState next = state_of(pair);
-    for (int i = pair; i < items && ok; i += pairs) {
-      const Item it = item_of<R>(i, ntile, n_heads, seq, key_lens);
+    for (int i = pair; i < items.total && ok; i += pairs) {
+      const Item it = items.at(i);
       const int row0 = it.tt * 2 * T + rank * T;
       if (it.nb == 0) {
         next = state_of(i + pairs);

@@ -136,6 +136,32 @@ def test_attention_padded(S, lens, hd, fmt):
             within(R.heads(g[b:b + 1, :n, i * d:(i + 1) * d], H), refs[i], tols[i], f"{name}, {n} of {S}")
 
 
+@pytest.mark.parametrize("S", [300, 250], ids=["two_tiles", "one_tile"])
+@pytest.mark.parametrize("which", ["mixed", "gap", "none"])
+def test_attention_gradient_of_many_elements(which, S):
+    """More elements than a warp has lanes, with runs that hold no tokens: each equals itself run alone."""
+    B, H, hd, fmt = 101, 3, 64, 0
+    d = H * hd
+    lens = [(37 * b) % (S + 1) for b in range(B)]
+    if which == "gap":  # nothing in elements 20 to 79, only single tokens at the end
+        lens = [0 if 20 <= b < 80 else 1 if b >= 95 else n for b, n in enumerate(lens)]
+    elif which == "none":
+        lens = [0] * (B - 1) + [S]
+    q, k, v, do = qkv_case(B, S, H, hd, fmt, 53)
+    kl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out, lse = run_forward(q, k, v, H, hd, fmt, kl)
+    g = run_backward(q, k, v, out, do, lse, H, hd, fmt, kl)
+    for b, n in enumerate(lens):
+        assert not g[b, n:].any()
+        if n == 0:
+            continue
+        q1, k1, v1, o1, do1 = (t[b:b + 1, :n] for t in (q, k, v, out, do))
+        refs, tols = R.attention_grad_bounds(*(R.heads(t, H) for t in (q1, k1, v1, o1, do1)),
+                                             lse[b:b + 1, :, :n].double(), fmt)
+        for i, name in enumerate(("dq", "dk", "dv")):
+            within(R.heads(g[b:b + 1, :n, i * d:(i + 1) * d], H), refs[i], tols[i], f"{name}, element {b}")
+
+
 def test_attention_negative_counts_are_no_tokens():
     q, k, v, do = qkv_case(2, 70, 1, 64, 0, 41)
     kl = torch.tensor([-3, 70], dtype=torch.int32, device="cuda")
