@@ -250,10 +250,16 @@ constexpr int bytes_of() {
   return F == FMT_F32 ? 4 : 2;
 }
 
-// Rows of up to 512 columns: a warp per row, V vectors of 8 per lane; the next row is loaded before the
-// current one's arithmetic.
+// Rows of up to 1024 columns: a warp per row, V vectors of 8 per lane; the next row is loaded before the
+// current one's arithmetic and kept as it is in memory.  HBM-bound: event-timed with the sums' kernel, L2
+// cold, 65536 rows: 1024 columns bf16 81 us (403 MB, 5.0 TB/s; the form for longer rows, whose CTA meets
+// once per row, 130), 512 bf16 48 us (4.2 TB/s), 256 bf16 31 us (3.2 TB/s) and fp32 with dres 52 us
+// (5.1 TB/s).  CTAs per SM: as many as hold the registers; at V = 1 three beat two in 16 bits (31 us
+// against 34) and lose to them in fp32 (54 against 52).
+constexpr int row_ctas(int v, bool fp32) { return v == 4 ? 1 : v == 2 || fp32 ? 2 : 3; }
+
 template <int V, int XF, int DF, int OF>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, row_ctas(V, XF == FMT_F32 || DF == FMT_F32))
     rmsnorm_bwd_warp_kernel(const void* __restrict__ x, const uint16_t* __restrict__ g, const void* __restrict__ dy,
                             const void* dres, void* dx, float* __restrict__ part, int64_t rows, int64_t cols,
                             float eps) {
@@ -262,38 +268,43 @@ __global__ void __launch_bounds__(256)
   const int nv = static_cast<int>(cols / 8), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float inv = 1.f / static_cast<float>(cols);
   const int64_t step = 8ll * gridDim.x;
-  float gv[V][8], acc[V][8], xn[V][8], yn[V][8];
+  // 8 values as they are in memory
+  constexpr int NX = bytes_of<XF>() / 2, NY = bytes_of<DF>() / 2;
+  uint4 gr[V], xr[V][NX], yr[V][NY];
+  float acc[V][8];
   auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int i = lane + 32 * j;
+      const int64_t i = row * nv + lane + 32 * j;
+      const bool in = lane + 32 * j < nv && row < rows;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) xn[j][k] = yn[j][k] = 0.f;
-      if (i < nv && row < rows) {
-        load8<XF>(x, row * nv + i, xn[j]);
-        load8<DF>(dy, row * nv + i, yn[j]);
-      }
+      for (int k = 0; k < NX; ++k) xr[j][k] = in ? reinterpret_cast<const uint4*>(x)[i * NX + k] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int k = 0; k < NY; ++k) yr[j][k] = in ? reinterpret_cast<const uint4*>(dy)[i * NY + k] : make_uint4(0u, 0u, 0u, 0u);
     }
   };
 #pragma unroll
   for (int j = 0; j < V; ++j) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) gv[j][k] = acc[j][k] = 0.f;
-    if (lane + 32 * j < nv) load8<FMT_BF16>(g, lane + 32 * j, gv[j]);
+    for (int k = 0; k < 8; ++k) acc[j][k] = 0.f;
+    gr[j] = lane + 32 * j < nv ? reinterpret_cast<const uint4*>(g)[lane + 32 * j] : make_uint4(0u, 0u, 0u, 0u);
   }
   fetch(blockIdx.x * 8ll + warp);
+#pragma unroll 1
   for (int64_t row = blockIdx.x * 8ll + warp; row < rows; row += step) {
     float xv[V][8], yv[V][8], e[V][8];
     float ss = 0.f, dot = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
+      load8<XF>(xr[j], 0, xv[j]);
+      load8<DF>(yr[j], 0, yv[j]);
+      float gv[8];
+      load8<FMT_BF16>(&gr[j], 0, gv);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        xv[j][k] = xn[j][k];
-        yv[j][k] = yn[j][k];
-        e[j][k] = 0.f;
         ss = fmaf(xv[j][k], xv[j][k], ss);
-        dot = fmaf(yv[j][k] * gv[j][k], xv[j][k], dot);
+        e[j][k] = 0.f;
+        dot = fmaf(yv[j][k] * gv[k], xv[j][k], dot);
       }
       if (dres != nullptr && lane + 32 * j < nv) load8<OF>(dres, row * nv + lane + 32 * j, e[j]);
     }
@@ -307,10 +318,12 @@ __global__ void __launch_bounds__(256)
     const float m = dot * inv * r * r;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
+      float gv[8];
+      load8<FMT_BF16>(&gr[j], 0, gv);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         acc[j][k] = fmaf(yv[j][k], xv[j][k] * r, acc[j][k]);
-        e[j][k] = fmaf(r, fmaf(-m, xv[j][k], yv[j][k] * gv[j][k]), e[j][k]);
+        e[j][k] = fmaf(r, fmaf(-m, xv[j][k], yv[j][k] * gv[k]), e[j][k]);
       }
       if (lane + 32 * j < nv) store8<OF>(dx, row * nv + lane + 32 * j, e[j]);
     }
@@ -327,8 +340,10 @@ __global__ void __launch_bounds__(256)
 }
 
 // Longer rows: a CTA per row at a time, V vectors of 8 per thread.  HBM-bound: x, dy and dres come
-// through a ring of bulk copies that keeps up to 200 KB in flight per SM (from registers, with one row
-// fetched ahead, 4608 x 4096 took 56 us against 47).  A stage is free for its next row when the CTA has
+// through a ring of bulk copies that keeps up to 200 KB in flight per SM.  With the sums' kernel, event-timed,
+// L2 cold: 4608 x 4096 fp32 rows with f16 dy 56 us (264 MB, 4.7 TB/s), bf16 41 us (151 MB, 3.6 TB/s), 16896 x 4096
+// bf16 109 us (5.1 TB/s), 4608 x 8192 bf16 58 us (5.2 TB/s).  From registers with one row fetched ahead the same took
+// 56, 44, 117 and 85 us.  A stage is free for its next row when the CTA has
 // met in the following row's reduction.
 template <int V, int XF, int DF, int OF>
 __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
@@ -448,15 +463,14 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
   }
 }
 
-// CTAs per SM of the long-row kernel, and the grid of both.
-static int norm_ctas_per_sm(int64_t cols) { return cols <= 1024 ? 4 : cols <= 4096 ? 2 : 1; }
-static int norm_grid(int64_t rows, int64_t cols) {
-  if (cols <= 512) {
-    const int64_t want = (rows + 7) / 8;
-    return static_cast<int>(want < 2 * SMS ? want : 2 * SMS);
-  }
-  const int64_t most = static_cast<int64_t>(SMS) * norm_ctas_per_sm(cols);
-  return static_cast<int>(rows < most ? rows : most);
+// CTAs per SM of the long-row kernel, and the grid of all forms.
+static int norm_ctas_per_sm(int64_t cols) { return cols <= 4096 ? 2 : 1; }
+static int norm_grid(int64_t rows, int64_t cols, bool fp32) {
+  const bool by_warps = cols <= 1024;
+  const int64_t want = by_warps ? (rows + 7) / 8 : rows;
+  const int64_t most =
+      static_cast<int64_t>(SMS) * (by_warps ? row_ctas(cols <= 256 ? 1 : cols <= 512 ? 2 : 4, fp32) : norm_ctas_per_sm(cols));
+  return static_cast<int>(want < most ? want : most);
 }
 
 template <int XF, int DF, int OF>
@@ -464,12 +478,13 @@ static cudaError_t launch_norm(const void* x, const uint16_t* g, const void* dy,
                                float* part, int64_t rows, int64_t cols, float eps, int grid, const KernelGuard& guard,
                                cudaStream_t s) {
   const int nv = static_cast<int>(cols / 8);
-  if (cols <= 256)
-    return launch_pdl(rmsnorm_bwd_warp_kernel<1, XF, DF, OF>, dim3(grid), dim3(256), 0, s, x, g, dy, dres, dx, part,
-                      rows, cols, eps);
-  if (cols <= 512)
-    return launch_pdl(rmsnorm_bwd_warp_kernel<2, XF, DF, OF>, dim3(grid), dim3(256), 0, s, x, g, dy, dres, dx, part,
-                      rows, cols, eps);
+  auto by_warps = [&](auto v) {
+    return launch_pdl(rmsnorm_bwd_warp_kernel<decltype(v)::value, XF, DF, OF>, dim3(grid), dim3(256), 0, s, x, g, dy, dres,
+                      dx, part, rows, cols, eps);
+  };
+  if (cols <= 256) return by_warps(std::integral_constant<int, 1>());
+  if (cols <= 512) return by_warps(std::integral_constant<int, 2>());
+  if (cols <= 1024) return by_warps(std::integral_constant<int, 4>());
   const int64_t stage = cols * (bytes_of<XF>() + bytes_of<DF>() + (dres != nullptr ? bytes_of<OF>() : 0));
   int64_t stages = 212 * 1024 / norm_ctas_per_sm(cols) / stage;
   stages = stages < 2 ? 2 : stages > MAX_STAGES ? MAX_STAGES : stages;
@@ -556,13 +571,13 @@ cudaError_t launch_qknorm_mrope_bwd(const void* qkv, Rows dqk, Rows dx, float* d
 }
 
 size_t rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
-  return static_cast<size_t>(tew::norm_grid(rows, cols)) * static_cast<size_t>(cols) * 4;
+  return static_cast<size_t>(tew::norm_grid(rows, cols, false)) * static_cast<size_t>(cols) * 4;  // no fewer CTAs than with fp32
 }
 
 cudaError_t launch_rmsnorm_bwd(const void* x, int x_fmt, const uint16_t* g, const void* dy, int dy_fmt,
                                const void* dres, void* dx, int dx_fmt, float* dg, int64_t rows, int64_t cols,
                                float eps, void* workspace, const KernelGuard& guard, cudaStream_t s) {
-  const int grid = tew::norm_grid(rows, cols);
+  const int grid = tew::norm_grid(rows, cols, x_fmt == FMT_F32 || dy_fmt == FMT_F32);
   float* part = static_cast<float*>(workspace);
   cudaError_t e;
   if (x_fmt == FMT_BF16)

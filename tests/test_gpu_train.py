@@ -410,7 +410,7 @@ def test_qk_backward_against_differences():
 
 
 @pytest.mark.parametrize("rows,cols", [(1, 8), (80, 256), (5, 264), (3, 4096), (700, 1000), (2, 4104), (601, 8192),
-                                       (1500, 512)])
+                                       (1500, 512), (2500, 1024), (1190, 776), (5000, 256), (400, 1032)])
 @pytest.mark.parametrize("xf,yf,of,res", [(0, 0, 0, True), (0, 1, 0, False), (2, 1, 2, True), (2, 2, 1, True),
                                           (0, 2, 2, False), (2, 0, 0, True)])
 def test_rmsnorm_backward(rows, cols, xf, yf, of, res):
