@@ -50,7 +50,14 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 }
 
 constexpr int MAX_STAGES = 8;
-constexpr int CTAS_PER_SM = 2;  // of the QK-norm gradient up to 256 threads a token
+
+// The QK-norm gradient's CTAs per SM: one above 256 threads a token, else what 96 registers a thread leave
+// room for (two at 256 threads and the two warps of angles).  A CTA works on one token at a time, so that
+// narrow models need many: event-timed with L2 cold, 4 x 4608 tokens of 4 or 8 heads of 64 77 us (two CTAs
+// 118; what is left is the angles' fp64), 2 x 4608 of 16 heads of 64 38 us (63) and of 128 58 us (69).
+constexpr int qk_ctas(int per_token) {
+  return per_token > 256 ? 1 : 65536 / (96 * ((per_token + 31) / 32 * 32 + 64));
+}
 
 // (b, s) of the tokens blockIdx.x, blockIdx.x + gridDim.x, ... without a division for each.
 struct TokenWalk {
@@ -76,10 +83,13 @@ struct TokenWalk {
 // together needed more registers than two CTAs of an SM have); thread layout as in the forward kernel,
 // one thread per head and 8 rotary pairs.  The last two warps run ahead: they copy a token's raw rows and
 // gradients into a ring of shared memory with two bulk copies and compute its angles beside them, an
-// angle per lane, so that the other warps wait for neither memory nor fp64.
+// angle per lane, so that the other warps wait for neither memory nor fp64.  4608 tokens x 32 heads of 128,
+// L2 cold: 52 us event-timed with the sums' kernel (226 MB, 4.4 TB/s); alone 46.6 us with instructions issued
+// in 65 % of the cycles, so it is bound by neither memory nor issue alone; with one warp of angles 58 us.
+// 16896 tokens 152 us (5.5 TB/s).
 // Tokens behind an element's count are not read; their gradients are zeros.
 template <int F, int HD, int MAX_THREADS>
-__global__ void __launch_bounds__(MAX_THREADS + 64, CTAS_PER_SM * 256 / MAX_THREADS)
+__global__ void __launch_bounds__(MAX_THREADS + 64, qk_ctas(MAX_THREADS))
     qknorm_mrope_bwd_kernel(const uint16_t* __restrict__ qkv, const uint16_t* dqk, int64_t ld_dqk, uint16_t* dx,
                             int64_t ld_dx, float* __restrict__ part, int64_t tokens, int seq, int n_heads, RopeArgs ra,
                             const uint16_t* __restrict__ g_q, const uint16_t* __restrict__ g_k, float eps, int stages,
@@ -515,7 +525,7 @@ static cudaError_t launch_norm_df(int dy_fmt, int dx_fmt, A... a) {
 
 // CTAs of the QK-norm gradient for each of q and k.
 static int qk_grid(int64_t tokens, int per_token) {
-  const int64_t most = (per_token <= 256 ? CTAS_PER_SM : CTAS_PER_SM / 2) * SMS / 2;
+  const int64_t most = qk_ctas(per_token) * SMS / 2;
   return static_cast<int>(tokens < most ? tokens : most);
 }
 
@@ -538,7 +548,7 @@ cudaError_t launch_qknorm_mrope_bwd(const void* qkv, Rows dqk, Rows dx, float* d
   const int grid = tew::qk_grid(tokens, per_token);
   // a stage holds the raw rows and their gradients; an SM's CTAs share about 190 KB
   const int stage = 4 * n_heads * head_dim;
-  int stages = 190 * 1024 / (per_token <= 256 ? tew::CTAS_PER_SM : tew::CTAS_PER_SM / 2) / stage;
+  int stages = 190 * 1024 / tew::qk_ctas(per_token) / stage;
   stages = stages < 2 ? 2 : stages > tew::MAX_STAGES ? tew::MAX_STAGES : stages;
   const int sums = warps * head_dim * 4;
   const int smem = stages * stage > sums ? stages * stage : sums;
