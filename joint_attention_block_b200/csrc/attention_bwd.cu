@@ -421,7 +421,7 @@ struct Ring {
   }
   __device__ __forceinline__ bool wait_empty(int u, const KernelGuard& g, volatile uint32_t* abort_flag,
                                              uint32_t where) const {
-    return mbar_wait(&empty[slot(u)], phase(u) ^ 1u, g, abort_flag, where);
+    return mbar_wait_warp(&empty[slot(u)], phase(u) ^ 1u, g, abort_flag, where);
   }
   // The leader arms the barrier for both CTAs' halves; returns its shared::cluster address.
   __device__ __forceinline__ uint32_t arm(int u, bool leader, uint32_t bytes) const {
@@ -520,6 +520,9 @@ struct Items {
 //   warp 1, leader    S(u) once S(u-1) has been read into registers, dP(u) likewise
 //   warp 2, leader    the products with P and dS, once those are written (warp 2 holds the TMEM)
 //   the others        the elementwise step; thread = own row and COLS columns of the block
+// A wait gives up after a limit.  Its warp then goes on to the end of the block (on whatever it finds; the
+// error word is set) and leaves by a vote of its lanes: leaving lane by lane could split the warp, and a vote
+// at every wait cost 3 %.  Only the loads ask at once, since they may not arm a barrier that is in use.
 // One lane of each issuing warp per pair runs the tensor cores of both SMs; with one warp for all
 // products its waits and commits took 1500 clocks a block, as long as the products.
 template <class L, int HD>
@@ -604,13 +607,12 @@ __device__ __forceinline__ void issue_s_dp(const Pipe<L, HD>& p, uint32_t t_s, u
   for (int i = pair; i < items.live && ok; i += pairs) {
     const int nb = items.at(i).nb;
     if (nb == 0) continue;
-    ok = p.at.wait_full(ui, guard, p.abort_flag, where(0, u));
+    ok = __all_sync(0xffffffffu, p.at.wait_full(ui, guard, p.abort_flag, where(0, u)));
     for (int j = 0; j < nb && ok; ++j, ++u) {
       const uint32_t prev = static_cast<uint32_t>(u - 1) & 1u;
       const uint8_t* slot = p.mem_a + (u % L::N) * L::SLOT_A;
-      ok = p.ra.wait_full(u, guard, p.abort_flag, where(1, u)) &&
-           (u == 0 || mbar_wait(p.s_empty, prev, guard, p.abort_flag, where(2, u)));
-      if (!ok) break;
+      ok &= p.ra.wait_full(u, guard, p.abort_flag, where(1, u));
+      ok &= u == 0 || mbar_wait(p.s_empty, prev, guard, p.abort_flag, where(2, u));
       tc_fence_after();
       if (one) {
         mma_rows<L, HD, F>(t_s, p.tile_a, slot);
@@ -618,9 +620,8 @@ __device__ __forceinline__ void issue_s_dp(const Pipe<L, HD>& p, uint32_t t_s, u
         if (j + 1 == nb) mma_commit_pair(&p.at.empty[0], 0x3);
       }
       __syncwarp();
-      ok = (j > 0 || p.bt.wait_full(ui, guard, p.abort_flag, where(3, u))) &&
-           (u == 0 || mbar_wait(p.dp_empty, prev, guard, p.abort_flag, where(4, u)));
-      if (!ok) break;
+      ok &= j > 0 || p.bt.wait_full(ui, guard, p.abort_flag, where(3, u));
+      ok &= u == 0 || mbar_wait(p.dp_empty, prev, guard, p.abort_flag, where(4, u));
       tc_fence_after();
       if (one) {
         mma_rows<L, HD, F>(t_dp, p.tile_b, slot + L::CUT);
@@ -628,7 +629,7 @@ __device__ __forceinline__ void issue_s_dp(const Pipe<L, HD>& p, uint32_t t_s, u
         mma_commit_pair(&p.ra.empty[u % L::N], 0x3);
         if (j + 1 == nb) mma_commit_pair(&p.bt.empty[0], 0x3);
       }
-      __syncwarp();
+      ok = __all_sync(0xffffffffu, ok);
     }
     ++ui;
   }
@@ -763,28 +764,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
         const int nb = items.at(i).nb;
         if (nb == 0) continue;
         // the first dV of an item overwrites accumulators that both CTAs must have read
-        ok = ui == 0 || mbar_wait(p.acc_empty, static_cast<uint32_t>(ui - 1) & 1u, guard, p.abort_flag, where(5, u));
+        ok = ui == 0 || mbar_wait_warp(p.acc_empty, static_cast<uint32_t>(ui - 1) & 1u, guard, p.abort_flag, where(5, u));
         for (int j = 0; j < nb && ok; ++j, ++u) {
           const uint32_t par = static_cast<uint32_t>(u) & 1u;
           const uint8_t* slot = p.mem_b + (u % N) * L::SLOT_B;
-          ok = p.rb.wait_full(u, guard, p.abort_flag, where(6, u)) &&
-               mbar_wait(p.p_full, par, guard, p.abort_flag, where(7, u));
-          if (!ok) break;
+          ok &= p.rb.wait_full(u, guard, p.abort_flag, where(6, u));
+          ok &= mbar_wait(p.p_full, par, guard, p.abort_flag, where(7, u));
           tc_fence_after();
           if (one) {
             mma_cols<L, HD, F>(tmem + C_DV, tmem + C_P, slot, j > 0);
             mma_commit_pair(p.p_empty, 0x3);
           }
           __syncwarp();
-          ok = mbar_wait(p.ds_full, par, guard, p.abort_flag, where(8, u));
-          if (!ok) break;
+          ok &= mbar_wait(p.ds_full, par, guard, p.abort_flag, where(8, u));
           tc_fence_after();
           if (one) {
             mma_cols<L, HD, F>(tmem + C_DK, tmem + C_DS, slot + L::CUT, j > 0);
             mma_commit_pair(p.ds_empty, 0x3);
             mma_commit_pair(&p.rb.empty[u % N], 0x3);
           }
-          __syncwarp();
+          ok = __all_sync(0xffffffffu, ok);
         }
         if (ok && one) mma_commit_pair(p.acc_full, 0x3);
         __syncwarp();
@@ -829,13 +828,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
       }
       // P carries 2^15 in f16; dS = that P times (dP - delta) times tau = 2^(shift - 15)
       const float tau = F == FMT_F16 ? exp2f(shift - P_SHIFT) : 1.f;
-      for (int j = 0; j < it.nb; ++j, ++u) {
+      for (int j = 0; j < it.nb && ok; ++j, ++u) {
         const uint32_t par = static_cast<uint32_t>(u) & 1u;
         const int sv = u % NV;
         const float* vec = p.vec + sv * 2 * R + COLS * part;
-        ok = mbar_wait(&p.vec_full[sv], static_cast<uint32_t>(u / NV) & 1u, guard, p.abort_flag, where(0, u)) &&
-             mbar_wait(p.s_full, par, guard, p.abort_flag, where(1, u));
-        if (!ok) break;
+        ok &= mbar_wait(&p.vec_full[sv], static_cast<uint32_t>(u / NV) & 1u, guard, p.abort_flag, where(0, u));
+        ok &= mbar_wait(p.s_full, par, guard, p.abort_flag, where(1, u));
         tc_fence_after();
         uint32_t raw[COLS];
         get_cols(s_col, raw);
@@ -850,14 +848,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
           e[k + 1] = ex2_approx(x.y);
           pk[k / 2] = pack2<F>(e[k], e[k + 1]);
         }
-        ok = mbar_wait(p.p_empty, par ^ 1u, guard, p.abort_flag, where(2, u));  // dV(u - 1) has read P
-        if (!ok) break;
+        ok &= mbar_wait(p.p_empty, par ^ 1u, guard, p.abort_flag, where(2, u));  // dV(u - 1) has read P
         tc_fence_after();
         put_cols(p_col, pk);
         tmem_st_wait();
         arrive(p.p_full);
-        ok = mbar_wait(p.dp_full, par, guard, p.abort_flag, where(3, u));
-        if (!ok) break;
+        ok &= mbar_wait(p.dp_full, par, guard, p.abort_flag, where(3, u));
         tc_fence_after();
         get_cols(dp_col, raw);
         got_cols(raw);
@@ -869,17 +865,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DkvLayout<HD>::THREA
           if constexpr (F == FMT_F16) y = mul2(y, make_float2(tau, tau));
           pk[k / 2] = pack2<F>(y.x, y.y);
         }
-        ok = mbar_wait(p.ds_empty, par ^ 1u, guard, p.abort_flag, where(4, u));  // dK(u - 1) has read dS
-        if (!ok) break;
+        ok &= mbar_wait(p.ds_empty, par ^ 1u, guard, p.abort_flag, where(4, u));  // dK(u - 1) has read dS
         tc_fence_after();
         put_cols(ds_col, pk);
         tmem_st_wait();
         arrive(p.ds_full);
+        ok = __all_sync(0xffffffffu, ok);
       }
       if (!ok) break;
       const float fv = F == FMT_F16 ? exp2f(-P_SHIFT) : 1.f, fk = scale * exp2f(-shift);
       shift = shift_of(i + pairs);  // the next item's, while the last products run
-      ok = mbar_wait(p.acc_full, static_cast<uint32_t>(ui) & 1u, guard, p.abort_flag, where(5, u));
+      ok = mbar_wait_warp(p.acc_full, static_cast<uint32_t>(ui) & 1u, guard, p.abort_flag, where(5, u));
       if (!ok) break;
       tc_fence_after();
       // 2 HD / OUT pieces of the rows (dV's, then dK's), dealt to the rows' warps in turn
@@ -995,18 +991,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DqLayout<HD>::THREAD
         const int nb = items.at(i).nb;
         if (nb == 0) continue;
         // the first dQ of an item overwrites an accumulator that both CTAs must have read
-        ok = ui == 0 || mbar_wait(p.acc_empty, static_cast<uint32_t>(ui - 1) & 1u, guard, p.abort_flag, where(9, u));
+        ok = ui == 0 || mbar_wait_warp(p.acc_empty, static_cast<uint32_t>(ui - 1) & 1u, guard, p.abort_flag, where(9, u));
         for (int j = 0; j < nb && ok; ++j, ++u) {
-          ok = p.rb.wait_full(u, guard, p.abort_flag, where(10, u)) &&
-               mbar_wait(p.ds_full, static_cast<uint32_t>(u) & 1u, guard, p.abort_flag, where(11, u));
-          if (!ok) break;
+          ok &= p.rb.wait_full(u, guard, p.abort_flag, where(10, u));
+          ok &= mbar_wait(p.ds_full, static_cast<uint32_t>(u) & 1u, guard, p.abort_flag, where(11, u));
           tc_fence_after();
           if (one) {
             mma_cols<L, HD, F>(tmem + C_DQ, tmem + C_DS, p.mem_b + (u % N) * L::SLOT_B, j > 0);
             mma_commit_pair(p.ds_empty, 0x3);
             mma_commit_pair(&p.rb.empty[u % N], 0x3);
           }
-          __syncwarp();
+          ok = __all_sync(0xffffffffu, ok);
         }
         if (ok && one) mma_commit_pair(p.acc_full, 0x3);
         __syncwarp();
@@ -1062,10 +1057,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DqLayout<HD>::THREAD
       const float2 nl2 = make_float2(nl, nl);
       // tau (dP - delta): one fma on the pair
       const float2 tau2 = make_float2(tau, tau), nd2 = make_float2(nd * tau, nd * tau);
-      for (int j = 0; j < it.nb; ++j, ++u) {
+      for (int j = 0; j < it.nb && ok; ++j, ++u) {
         const uint32_t par = static_cast<uint32_t>(u) & 1u;
-        ok = mbar_wait(p.s_full, par, guard, p.abort_flag, where(6, u));
-        if (!ok) break;
+        ok &= mbar_wait(p.s_full, par, guard, p.abort_flag, where(6, u));
         tc_fence_after();
         uint32_t raw[COLS];
         get_cols(s_col, raw);
@@ -1078,8 +1072,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DqLayout<HD>::THREAD
           e[k] = ex2_approx(x.x);
           e[k + 1] = ex2_approx(x.y);
         }
-        ok = mbar_wait(p.dp_full, par, guard, p.abort_flag, where(7, u));
-        if (!ok) break;
+        ok &= mbar_wait(p.dp_full, par, guard, p.abort_flag, where(7, u));
         tc_fence_after();
         get_cols(dp_col, raw);
         got_cols(raw);
@@ -1099,16 +1092,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(DqLayout<HD>::THREAD
           const float2 y = mul2(F == FMT_F16 ? fma2(v, tau2, nd2) : add2(v, nd2), make_float2(e[k], e[k + 1]));
           pk[k / 2] = pack2<F>(y.x, y.y);
         }
-        ok = mbar_wait(p.ds_empty, par ^ 1u, guard, p.abort_flag, where(8, u));  // dQ(u - 1) has read dS
-        if (!ok) break;
+        ok &= mbar_wait(p.ds_empty, par ^ 1u, guard, p.abort_flag, where(8, u));  // dQ(u - 1) has read dS
         tc_fence_after();
         put_cols(ds_col, pk);
         tmem_st_wait();
         arrive(p.ds_full);
+        ok = __all_sync(0xffffffffu, ok);
       }
       if (!ok) break;
       next = state_of(i + pairs);  // while the last products run
-      ok = mbar_wait(p.acc_full, static_cast<uint32_t>(ui) & 1u, guard, p.abort_flag, where(9, u));
+      ok = mbar_wait_warp(p.acc_full, static_cast<uint32_t>(ui) & 1u, guard, p.abort_flag, where(9, u));
       if (!ok) break;
       tc_fence_after();
       const float fq = scale * exp2f(-shift);

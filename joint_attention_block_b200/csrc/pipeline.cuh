@@ -1,4 +1,4 @@
-// One lane of a converged warp, chosen by the hardware.
+// What the roles of a warp-specialised kernel share: one elected lane, and waits of whole warps.
 #pragma once
 
 #include "common.cuh"
@@ -13,6 +13,14 @@ JAB_DEVICE bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
   return p != 0;
+}
+
+// mbar_wait by a whole warp, with one verdict for all lanes: after a wait that gave up in some lanes only
+// (the phase completed between their last looks) the warp would split and its next warp-wide step never end.
+JAB_DEVICE bool mbar_wait_warp(uint64_t* bar, uint32_t parity, const KernelGuard& g, volatile uint32_t* abort_flag,
+                               uint32_t where) {
+  const bool ok = mbar_wait(bar, parity, g, abort_flag, where);
+  return __all_sync(0xffffffffu, ok);
 }
 
 }  // namespace jab

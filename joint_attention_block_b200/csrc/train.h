@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "internal.h"
 
@@ -73,16 +74,22 @@ cudaError_t launch_rmsnorm_bwd(const void* x, int x_fmt, const uint16_t* g, cons
                                float eps, void* workspace, const KernelGuard& guard, cudaStream_t s);
 
 // Let a kernel have `bytes` of dynamic shared memory, once per device and size: the call costs about a
-// microsecond, which the smallest sizes notice.
+// microsecond, which the smallest sizes notice.  The allowance only grows, under a lock, so that one thread
+// cannot lower what another has just asked for.
 template <auto Kernel>
 cudaError_t allow_smem(int bytes) {
-  static std::atomic<int> set[64];
+  constexpr int DEVICES = 64;
+  static std::atomic<int> set[DEVICES];
+  static std::mutex growing;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64 && set[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+  if (dev < 0 || dev >= DEVICES) return cudaErrorInvalidDevice;
+  if (set[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+  const std::lock_guard<std::mutex> lock(growing);
+  if (set[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev >= 0 && dev < 64) set[dev].store(bytes, std::memory_order_relaxed);
+  if (e == cudaSuccess) set[dev].store(bytes, std::memory_order_release);
   return e;
 }
 

@@ -53,8 +53,8 @@ constexpr int MAX_STAGES = 8;
 
 // The QK-norm gradient's CTAs per SM: one above 256 threads a token, else what 96 registers a thread leave
 // room for (two at 256 threads and the two warps of angles).  A CTA works on one token at a time, so that
-// narrow models need many: event-timed with L2 cold, 4 x 4608 tokens of 4 or 8 heads of 64 77 us (two CTAs
-// 118; what is left is the angles' fp64), 2 x 4608 of 16 heads of 64 38 us (63) and of 128 58 us (69).
+// narrow models need many: event-timed with L2 cold, 4 x 4608 tokens of 4 or 8 heads of 64 79 us (two CTAs
+// 118; what is left is the angles' fp64), 2 x 4608 of 16 heads of 64 39 us (63) and of 128 59 us (69).
 constexpr int qk_ctas(int per_token) {
   return per_token > 256 ? 1 : 65536 / (96 * ((per_token + 31) / 32 * 32 + 64));
 }
@@ -86,7 +86,7 @@ struct TokenWalk {
 // angle per lane, so that the other warps wait for neither memory nor fp64.  4608 tokens x 32 heads of 128,
 // L2 cold: 52 us event-timed with the sums' kernel (226 MB, 4.4 TB/s); alone 46.6 us with instructions issued
 // in 65 % of the cycles, so it is bound by neither memory nor issue alone; with one warp of angles 58 us.
-// 16896 tokens 152 us (5.5 TB/s).
+// 16896 tokens 154 us (5.4 TB/s).
 // Tokens behind an element's count are not read; their gradients are zeros.
 template <int F, int HD, int MAX_THREADS>
 __global__ void __launch_bounds__(MAX_THREADS + 64, qk_ctas(MAX_THREADS))
@@ -127,10 +127,9 @@ __global__ void __launch_bounds__(MAX_THREADS + 64, qk_ctas(MAX_THREADS))
       int pt, ph, pw;
       rope_position(ra, b, s, pt, ph, pw);
       const int st = u % stages;
-      if (!mbar_wait(&empty[st], (static_cast<uint32_t>(u / stages) & 1u) ^ 1u, guard, &abort_flag,
-                     where_code(ERR_TIMEOUT_QKBWD, 0, u)))
-        break;
-      if (first && lane == 0) {
+      const bool got = mbar_wait(&empty[st], (static_cast<uint32_t>(u / stages) & 1u) ^ 1u, guard, &abort_flag,
+                                 where_code(ERR_TIMEOUT_QKBWD, 0, u));
+      if (first && lane == 0 && got) {
         // the angles below are part of the phase: its two arrivals come after them
         asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&full[st])),
                      "r"(2 * row_bytes)
@@ -140,9 +139,10 @@ __global__ void __launch_bounds__(MAX_THREADS + 64, qk_ctas(MAX_THREADS))
       }
       if (const int i = first ? lane : lane + 32; i < half)
         rope_angle(ra, i, i < ra.sec_t ? pt : (i < ra.sec_t + ra.sec_h ? ph : pw), s_cos[st][i], s_sin[st][i]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[st]);
+      const bool all = __all_sync(0xffffffffu, got);
+      if (lane == 0 && got) mbar_arrive(&full[st]);
       ++u;
+      if (!all) break;  // a wait gave up: the warp leaves as a whole
     }
     // never leave with copies in flight
     if (first) {
@@ -222,9 +222,9 @@ __global__ void __launch_bounds__(MAX_THREADS + 64, qk_ctas(MAX_THREADS))
       continue;
     }
     const int st = u % stages;
-    if (!mbar_wait(&full[st], static_cast<uint32_t>(u / stages) & 1u, guard, &abort_flag,
-                   where_code(ERR_TIMEOUT_QKBWD, 2, u)))
-      break;
+    // a wait that gave up has set the error word and every later one gives up soon; the warp's lanes go on
+    // together, since they meet in every token's reduction
+    mbar_wait(&full[st], static_cast<uint32_t>(u / stages) & 1u, guard, &abort_flag, where_code(ERR_TIMEOUT_QKBWD, 2, u));
     const uint16_t* x = reinterpret_cast<const uint16_t*>(ring + st * 2 * row_bytes) + h * HD + 8 * c;
     one(x, x + d, out, s_cos[st], s_sin[st]);
     __syncwarp();
@@ -401,11 +401,12 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
     if (i < nv) load8<FMT_BF16>(g, i, gv[j]);
   }
   int u = 0;
+  bool ok = true;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, ++u) {
     const int st = u % stages, buf = u & 1;
-    if (!mbar_wait(&full[st], static_cast<uint32_t>(u / stages) & 1u, guard, &abort_flag,
-                   where_code(ERR_TIMEOUT_NORMBWD, 0, u)))
-      break;
+    // a wait that gave up has set the error word; the CTA's threads go on together, since all of them meet
+    // in every row's reduction, but load no more
+    ok &= mbar_wait(&full[st], static_cast<uint32_t>(u / stages) & 1u, guard, &abort_flag, where_code(ERR_TIMEOUT_NORMBWD, 0, u));
     const uint8_t* at = ring + static_cast<size_t>(st) * stage_bytes;
     float xv[V][8], yv[V][8];
     float ss = 0.f, dot = 0.f;
@@ -432,7 +433,7 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
     if (lane == 0) red[buf][warp] = make_float2(ss, dot);
     __syncthreads();  // two buffers: the next row's writes cannot meet this row's reads
     // the CTA is done with the row before this one: its stage takes the row `stages` after it
-    if (threadIdx.x == 0 && u > 0) {
+    if (threadIdx.x == 0 && u > 0 && ok) {
       const int64_t ahead = row + (stages - 1) * static_cast<int64_t>(gridDim.x);
       if (ahead < rows) load(ahead);
     }
