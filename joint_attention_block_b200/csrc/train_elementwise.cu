@@ -401,12 +401,12 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
     if (i < nv) load8<FMT_BF16>(g, i, gv[j]);
   }
   int u = 0;
-  bool ok = true;
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, ++u) {
     const int st = u % stages, buf = u & 1;
-    // a wait that gave up has set the error word; the CTA's threads go on together, since all of them meet
-    // in every row's reduction, but load no more
-    ok &= mbar_wait(&full[st], static_cast<uint32_t>(u / stages) & 1u, guard, &abort_flag, where_code(ERR_TIMEOUT_NORMBWD, 0, u));
+    // a thread whose wait gave up meets no other on its way out: the row's barrier waits for those that stay
+    if (!mbar_wait(&full[st], static_cast<uint32_t>(u / stages) & 1u, guard, &abort_flag,
+                   where_code(ERR_TIMEOUT_NORMBWD, 0, u)))
+      break;
     const uint8_t* at = ring + static_cast<size_t>(st) * stage_bytes;
     float xv[V][8], yv[V][8];
     float ss = 0.f, dot = 0.f;
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
     if (lane == 0) red[buf][warp] = make_float2(ss, dot);
     __syncthreads();  // two buffers: the next row's writes cannot meet this row's reads
     // the CTA is done with the row before this one: its stage takes the row `stages` after it
-    if (threadIdx.x == 0 && u > 0 && ok) {
+    if (threadIdx.x == 0 && u > 0) {
       const int64_t ahead = row + (stages - 1) * static_cast<int64_t>(gridDim.x);
       if (ahead < rows) load(ahead);
     }
