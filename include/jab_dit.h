@@ -315,8 +315,9 @@ DIT_API int dit_joint_attention(const void* qkv, void* out, int fmt, int batch, 
  *
  * Row views: a pointer with a leading dimension ld (elements) is a 16-bit [batch, seq, cols] view
  * whose rows are ld apart and whose batch elements are seq * ld apart; ld >= cols, ld % 8 == 0,
- * 16-byte aligned; the attention calls return UNSUPPORTED for seq * ld >= 2^39.  q and k inside [B, S, 2d], v inside the fused [B, S, 3d], and the gradients
- * inside one [B, S, 3d] buffer are such views.
+ * 16-byte aligned; the attention calls return UNSUPPORTED for seq * ld >= 2^39.  q and k inside
+ * [B, S, 2d], v inside the fused [B, S, 3d], and the gradients inside one [B, S, 3d] buffer are such
+ * views.
  * Padded batches: key_lens (DEVICE int32 [batch], clamped to [0, seq]; NULL: all rows) gives the
  * leading rows of each element that take part, as queries and as keys.  The rows behind them are
  * never used, whatever they hold (NaN included); their outputs and gradients are written as zeros.

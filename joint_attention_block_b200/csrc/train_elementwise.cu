@@ -13,7 +13,8 @@ namespace tew {
 
 constexpr int SMS = 148;  // grids are multiples of it; the workspaces hold a partial row per CTA
 
-// dst[c] = sum over the n rows of part [n, cols]; one CTA per 32 columns, 32 row lanes each.
+// dst[c] = sum over the n rows of part [n, cols]; one CTA per 32 columns, 32 row lanes each.  Latency-bound:
+// 296 rows of 4096 columns (4.8 MB, from L2) 5.7 us, 148 rows of 256 columns 4.9 us.
 __global__ void __launch_bounds__(1024) sum_rows_kernel(const float* __restrict__ part, int n, int64_t cols,
                                                         float* __restrict__ dst0, float* __restrict__ dst1,
                                                         int64_t split) {
