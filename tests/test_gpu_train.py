@@ -458,3 +458,89 @@ def test_rmsnorm_backward_against_differences():
         e = mine.double() / mine.double().norm()
         diff = (up(h * e) - up(-h * e)) / (2 * h)
         assert abs(diff - mine.double().norm().item()) <= 1e-5 * abs(diff)
+
+
+# ---------------------------------------------------------------- both, as a program uses them
+
+
+def test_elementwise_gradients_on_other_streams_and_in_graphs():
+    """Two streams with their own workspaces, then a captured run replayed on other inputs: the same bits."""
+    B, n_text, gh, gw, H, hd, fmt = 2, 30, 8, 8, 4, 64, 0
+    cfg, (gq, gk), d, S = config(H, hd), gains(5, hd), H * hd, n_text + gh * gw
+    g = gen(67)
+    tl = torch.tensor([30, 11], dtype=torch.int32, device="cuda")
+    gain = torch.ones(d, device="cuda").bfloat16()
+    qkv, dqk = randn(g, B, S, 3 * d, fmt=fmt), randn(g, B, S, 2 * d, std=0.02, fmt=fmt)
+    x, dy = randn(g, B * S, d, fmt=2), randn(g, B * S, d, std=0.02, fmt=fmt)
+
+    def results():
+        return [nan_like(B, S, 2 * d, fmt=fmt), nan_like(B, S, 2 * d, fmt=fmt), nan_like(hd, fmt=2), nan_like(hd, fmt=2),
+                nan_like(B * S, d, fmt=2), nan_like(d, fmt=2)]
+
+    def works():
+        return (ws(ops.qknorm_mrope_backward_workspace_bytes(cfg, B, S)),
+                ws(ops.rmsnorm_rows_backward_workspace_bytes(B * S, d)))
+
+    def run(r, w, stream=None):
+        ops.qknorm_mrope_out(qkv, r[0], cfg, n_text, gh, gw, gq, gk, text_lens=tl, fmt=fmt, stream=stream)
+        ops.qknorm_mrope_backward(qkv, dqk, r[1], cfg, n_text, gh, gw, gq, gk, r[2], r[3], w[0], text_lens=tl, fmt=fmt,
+                                  stream=stream)
+        ops.rmsnorm_rows_backward(x, gain, dy, r[4], r[5], 1e-6, w[1], x_fmt=2, dy_fmt=fmt, dx_fmt=2, stream=stream)
+
+    ref = results()
+    run(ref, works())
+    streams, got, wss = [torch.cuda.Stream() for _ in range(2)], [results() for _ in range(2)], [works() for _ in range(2)]
+    torch.cuda.synchronize()
+    for s, r, w in zip(streams, got, wss):
+        run(r, w, s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for r in got for a, b in zip(r, ref))
+    graph, mine = torch.cuda.CUDAGraph(), results()
+    with torch.cuda.graph(graph):
+        run(mine, wss[0])
+    qkv.copy_(randn(g, B, S, 3 * d, fmt=fmt))
+    x.copy_(randn(g, B * S, d, fmt=2))
+    tl.copy_(torch.tensor([0, 29], dtype=torch.int32))
+    graph.replay()
+    run(ref, wss[1])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(mine, ref))
+
+
+def test_elementwise_offsets_past_32_bits():
+    """Buffers of more than 2^32 bytes and 2^31 elements: the last tokens and rows equal a short run."""
+    H, hd, fmt, n = 64, 128, 0, 512
+    cfg, (gq, gk), d = config(H, hd), gains(7, hd), H * hd
+    B = (1 << 31) // (3 * d * n) + 1
+    g = gen(71)
+    qkv = torch.zeros(B, n, 3 * d, dtype=DT[fmt], device="cuda")
+    grad = torch.zeros_like(qkv)
+    qkv[-1], grad[-1] = randn(g, n, 3 * d, fmt=fmt), randn(g, n, 3 * d, std=0.02, fmt=fmt)
+    one, gone, dq1 = qkv[-1:].clone(), grad[-1:].clone(), grad[-1:].clone()
+    qk, qk1 = torch.empty(B, n, 2 * d, dtype=DT[fmt], device="cuda"), nan_like(1, n, 2 * d, fmt=fmt)
+    ops.qknorm_mrope_out(qkv, qk, cfg, n, 0, 0, gq, gk, fmt=fmt)
+    ops.qknorm_mrope_out(one, qk1, cfg, n, 0, 0, gq, gk, fmt=fmt)
+    assert torch.equal(qk[-1:], qk1)
+    del qk
+    dg, dg1 = [nan_like(hd, fmt=2) for _ in range(2)], [nan_like(hd, fmt=2) for _ in range(2)]
+    for a, b, c in ((qkv, grad, dg), (one, gone, dg1)):
+        ops.qknorm_mrope_backward(a, b[..., :2 * d], b[..., :2 * d], cfg, n, 0, 0, gq, gk, *c,
+                                  ws(ops.qknorm_mrope_backward_workspace_bytes(cfg, a.shape[0], n)), fmt=fmt)
+    assert torch.equal(grad[-1:], gone)
+    # zero gradients before the last element add nothing; each sum is within its chains (as above) of the exact one
+    ang = R.angles(R.positions(n, 0, 0, -1, n, "cuda")[None], cfg.rope_sections, cfg.rope_theta, hd)
+    for w, gain in enumerate((gq, gk)):
+        x, dy = (t[..., w * d:(w + 1) * d].double().view(1, n, H, hd) for t in (one, dq1))
+        _, term, _, tsize = R.qk_backward(x, gain.double(), ang, cfg.eps, dy)
+        for got in (dg[w], dg1[w]):
+            within(got, term.sum((0, 1, 2)), (n / 100 + 96) * 2.0 ** -24 * tsize.sum((0, 1, 2)) + 1e-30, f"dg[{w}]")
+    del qkv, grad
+    rows, cols = (1 << 31) // 8192 + 9, 8192
+    x, dy = torch.zeros(rows, cols, dtype=DT[fmt], device="cuda"), torch.zeros(rows, cols, dtype=DT[fmt], device="cuda")
+    x[-5:], dy[-5:] = randn(g, 5, cols, fmt=fmt), randn(g, 5, cols, std=0.02, fmt=fmt)
+    gain = torch.ones(cols, device="cuda").bfloat16()
+    xs, dys, dx1 = x[-5:].clone(), dy[-5:].clone(), nan_like(5, cols, fmt=fmt)
+    dx, dgn = dy.clone(), nan_like(cols, fmt=2)
+    ops.rmsnorm_rows_backward(x, gain, dy, dx, dgn, 1e-6, ws(ops.rmsnorm_rows_backward_workspace_bytes(rows, cols)))
+    ops.rmsnorm_rows_backward(xs, gain, dys, dx1, dgn.clone(), 1e-6, ws(ops.rmsnorm_rows_backward_workspace_bytes(5, cols)))
+    assert torch.equal(dx[-5:], dx1) and not dx[:-5].any()
