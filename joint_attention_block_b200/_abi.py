@@ -372,8 +372,13 @@ def joint_attention_e4m3(q8: torch.Tensor, k8: torch.Tensor, scale: torch.Tensor
 
 # ---------------------------------------------------------------- training pass of the attention sublayer
 
-_FMT_DTYPES = {FMT_BF16: (torch.bfloat16, torch.int16, torch.uint16), FMT_F16: (torch.float16, torch.int16, torch.uint16),
-               FMT_F32: (torch.float32,)}
+class _FormatTypes(dict):
+    def __missing__(self, fmt):
+        raise ValueError(f"unknown fmt {fmt}")
+
+
+_FMT_DTYPES = _FormatTypes({FMT_BF16: (torch.bfloat16, torch.int16, torch.uint16),
+                            FMT_F16: (torch.float16, torch.int16, torch.uint16), FMT_F32: (torch.float32,)})
 
 
 def _on_device(**tensors) -> None:

@@ -136,6 +136,14 @@ def test_binding_checks_types_shapes_strides_and_devices(cfg):
         _abi.rmsnorm_rows_backward(x, t(64), x, x, t(64, dt=torch.float32), 1e-6, x, dx_fmt=2, stream=0)
 
 
+def test_unknown_formats_are_value_errors(cfg):
+    x, f = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(64)
+    with pytest.raises(ValueError, match="unknown fmt 7"):
+        _abi.rmsnorm_rows_backward(x, x[0], x, x, f, 1e-6, x, x_fmt=7, stream=0)
+    with pytest.raises(ValueError, match="unknown fmt -1"):
+        _abi.qknorm_mrope_out(x, x, cfg, 16, 8, 8, x, x, fmt=-1, stream=0)
+
+
 def test_single_row_views_have_a_leading_dimension():
     """The stride of a length-one dimension is arbitrary; the binding takes the one that addresses something."""
     d = 128
