@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(512, 2)  // <= 64 registers: four 256-thread C
     const int count = rope_position(ra, b, s, pt, ph, pw);
     if (ra.kv_len != nullptr && s == 0 && threadIdx.x == 0) ra.kv_len[b] = count;
     for (int i = threadIdx.x; i < half; i += blockDim.x)
-      rope_angle(ra, i, i < ra.sec_t ? pt : (i < ra.sec_t + ra.sec_h ? ph : pw), s_cos[i], s_sin[i]);
+      rope_angle(ra.inv_freq[i], i < ra.sec_t ? pt : (i < ra.sec_t + ra.sec_h ? ph : pw), s_cos[i], s_sin[i]);
   }
   if constexpr (Q8) {
     if (threadIdx.x < 32) {  // max |g| of both gains, hd <= 128 values each: four per lane

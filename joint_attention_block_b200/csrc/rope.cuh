@@ -79,8 +79,8 @@ __device__ __forceinline__ int rope_position(const RopeArgs& ra, int b, int s, i
 // Cosine and sine of pair i's angle at position p on its axis: p * inv_freq_i is exact in fp64; it is
 // reduced by the nearest multiple of 2 pi in fp64 (error ~1e-13 for the angles of any image),
 // rounded once to fp32 in [-pi, pi], and its sine and cosine taken in fp32.
-__device__ __forceinline__ void rope_angle(const RopeArgs& ra, int i, int p, float& cs, float& sn) {
-  const double x = static_cast<double>(p) * static_cast<double>(ra.inv_freq[i]);
+__device__ __forceinline__ void rope_angle(float inv_freq, int p, float& cs, float& sn) {
+  const double x = static_cast<double>(p) * static_cast<double>(inv_freq);
   const double k = rint(x * 0.15915494309189535);
   const float r = static_cast<float>(fma(-k, 6.283185307179586, x));
   sincosf(r, &sn, &cs);

@@ -52,12 +52,13 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 constexpr int MAX_STAGES = 8;
 
-// The QK-norm gradient's CTAs per SM: one above 256 threads a token, else what 96 registers a thread leave
-// room for (two at 256 threads and the two warps of angles).  A CTA works on one token at a time, so that
-// narrow models need many: event-timed with L2 cold, 4 x 4608 tokens of 4 or 8 heads of 64 79 us (two CTAs
-// 118; what is left is the angles' fp64), 2 x 4608 of 16 heads of 64 39 us (63) and of 128 59 us (69).
+// The QK-norm gradient's CTAs per SM: one above 256 threads a token, else what fits with 96 registers a
+// thread, of which an SM's four quarters hold five warps each (two CTAs of 256 threads and the two warps of
+// angles).  A CTA works on one token at a time, so that
+// narrow models need many: event-timed with L2 cold, 4 x 4608 tokens of 4 or 8 heads of 64 54 us (two CTAs
+// 118, seven, one of them in a second wave, 70), 2 x 4608 of 16 heads of 64 38 us (63) and of 128 58 us (69).
 constexpr int qk_ctas(int per_token) {
-  return per_token > 256 ? 1 : 65536 / (96 * ((per_token + 31) / 32 * 32 + 64));
+  return per_token > 256 ? 1 : 20 / ((per_token + 31) / 32 + 2);
 }
 
 // (b, s) of the tokens blockIdx.x, blockIdx.x + gridDim.x, ... without a division for each.
@@ -87,7 +88,7 @@ struct TokenWalk {
 // angle per lane, so that the other warps wait for neither memory nor fp64.  4608 tokens x 32 heads of 128,
 // L2 cold: 52 us event-timed with the sums' kernel (226 MB, 4.4 TB/s); alone 46.6 us with instructions issued
 // in 65 % of the cycles, so it is bound by neither memory nor issue alone; with one warp of angles 58 us.
-// 16896 tokens 154 us (5.4 TB/s).
+// 16896 tokens 150 us (5.5 TB/s).
 // Tokens behind an element's count are not read; their gradients are zeros.
 template <int F, int HD, int MAX_THREADS>
 __global__ void __launch_bounds__(MAX_THREADS + 64, qk_ctas(MAX_THREADS))
@@ -120,6 +121,11 @@ __global__ void __launch_bounds__(MAX_THREADS + 64, qk_ctas(MAX_THREADS))
 
   if (warp >= warps) {
     const bool first = warp == warps;
+    // this lane's pair: its frequency and axis, once for all tokens (read per token, from where the lanes'
+    // addresses differ, 16896 tokens of 32 heads of 128 took 155 us against 150)
+    const int i = first ? lane : lane + 32;
+    const float freq = i < half ? ra.inv_freq[i] : 0.f;
+    const int axis = i < ra.sec_t ? 0 : i < ra.sec_t + ra.sec_h ? 1 : 2;
     int u = 0;
     TokenWalk w(seq);
     for (int64_t bs = blockIdx.x; bs < tokens; bs += gridDim.x, w.step(seq)) {
@@ -138,8 +144,7 @@ __global__ void __launch_bounds__(MAX_THREADS + 64, qk_ctas(MAX_THREADS))
         bulk_load(ring + st * 2 * row_bytes, qkv + bs * 3 * d + col, row_bytes, &full[st]);
         bulk_load(ring + st * 2 * row_bytes + row_bytes, dqk + bs * ld_dqk + col, row_bytes, &full[st]);
       }
-      if (const int i = first ? lane : lane + 32; i < half)
-        rope_angle(ra, i, i < ra.sec_t ? pt : (i < ra.sec_t + ra.sec_h ? ph : pw), s_cos[st][i], s_sin[st][i]);
+      if (i < half) rope_angle(freq, axis == 0 ? pt : axis == 1 ? ph : pw, s_cos[st][i], s_sin[st][i]);
       const bool all = __all_sync(0xffffffffu, got);
       if (lane == 0 && got) mbar_arrive(&full[st]);
       ++u;
