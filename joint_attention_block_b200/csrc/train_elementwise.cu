@@ -145,8 +145,10 @@ __global__ void __launch_bounds__(MAX_THREADS + 64, qk_ctas(MAX_THREADS))
         bulk_load(ring + st * 2 * row_bytes + row_bytes, dqk + bs * ld_dqk + col, row_bytes, &full[st]);
       }
       if (i < half) rope_angle(freq, axis == 0 ? pt : axis == 1 ? ph : pw, s_cos[st][i], s_sin[st][i]);
-      const bool all = __all_sync(0xffffffffu, got);
+      // the lanes' stores come before lane 0's release; the vote below orders no memory
+      __syncwarp();
       if (lane == 0 && got) mbar_arrive(&full[st]);
+      const bool all = __all_sync(0xffffffffu, got);
       ++u;
       if (!all) break;  // a wait gave up: the warp leaves as a whole
     }
