@@ -5,7 +5,8 @@ import torch
 
 import train_ref as R
 from joint_attention_block_b200 import ops
-from test_gpu_train import FMTS, _clean_errors, qk_backward_case  # noqa: F401
+from test_gpu_train import FMTS, _clean_errors, qk_backward_case, qkv_case  # noqa: F401
+from train_ref import nan_like, run_backward, run_forward, ws
 
 pytestmark = pytest.mark.gpu
 
@@ -20,3 +21,31 @@ def test_qk_backward_of_many_tokens_per_cta(B, H, hd, padded, fmt):
     n_text, gh, gw = 40, 5, 15
     lens = [(17 * b) % (n_text + 1) for b in range(B)] if padded else None
     qk_backward_case(B, n_text, gh, gw, H, hd, fmt, 107 + B, lens=lens)
+
+
+@FMTS
+@pytest.mark.parametrize("S,H,hd", [(520, 4, 128), (520, 4, 64), (90, 3, 64)])
+def test_attention_gradients_in_a_row_in_one_workspace(S, H, hd, fmt):
+    """Inputs, lengths and workspace written and read by call after call without a pause: every call sees what its
+    own inputs' kernels and its own preparation wrote, so it equals the same call by itself in a fresh workspace."""
+    B, calls, d = 3, 10, H * hd
+    w = ws(ops.joint_attention_backward_workspace_bytes(B, S, H, hd))
+    cases, refs = [], []
+    for i in range(calls):
+        q, k, v, do = (t.contiguous() for t in qkv_case(B, S, H, hd, fmt, 400 + i, do_std=10.0 ** (i % 3 - 2)))
+        lens = torch.tensor([(131 * (i + b) + 17 * b) % (S + 1) for b in range(B)], dtype=torch.int32, device="cuda")
+        out, lse = run_forward(q, k, v, H, hd, fmt, lens)
+        cases.append((q, k, v, out, do, lse, lens))
+        refs.append(run_backward(q, k, v, out, do, lse, H, hd, fmt, lens))
+    bufs = [torch.empty_like(t) for t in cases[0]]
+    got = [nan_like(B, S, 3 * d, fmt=fmt) for _ in range(calls)]
+    torch.cuda.synchronize()
+    for case, g in zip(cases, got):
+        for dst, src in zip(bufs, case):
+            dst.copy_(src)
+        q, k, v, out, do, lse, lens = bufs
+        ops.joint_attention_backward(q, k, v, out, do, lse, g[..., :d], g[..., d:2 * d], g[..., 2 * d:], H, hd, w,
+                                     key_lens=lens, fmt=fmt)
+    torch.cuda.synchronize()
+    for i, (g, ref) in enumerate(zip(got, refs)):
+        assert torch.equal(g, ref), i
