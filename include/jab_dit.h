@@ -376,8 +376,8 @@ DIT_API size_t dit_joint_attention_backward_workspace_bytes(int batch, int seq, 
  *   dS = P (dP - delta) / sqrt(hd), dq = dS k, dk = dS^T q, dv = P^T dout.
  * out, lse: as the forward wrote them; dout: [batch, seq, d] in fmt; dq, dk, dv: row views of d
  * columns in fmt, no overlap with an input.  P and dS are rounded to fmt for the products (in F16
- * under a power-of-two scale taken from the data, so small gradients do not vanish below f16's
- * range); every sum is fp32.
+ * under powers of two taken from the data, for dq one per row of dout and for dk one per head, so
+ * small gradients do not vanish below f16's range); every sum is fp32.
  * Errors: as dit_joint_attention_lse; WORKSPACE (always needed). */
 DIT_API int dit_joint_attention_backward(const void* q, int64_t ld_q, const void* k, int64_t ld_k, const void* v,
                                          int64_t ld_v, const void* out, const void* dout, const float* lse, void* dq,

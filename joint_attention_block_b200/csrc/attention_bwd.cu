@@ -20,9 +20,12 @@
 // Roundings.  S, dP and all sums are fp32.  P and dS are rounded once to the inputs' 16-bit format,
 // the operand type of the products they enter.  In f16 they are scaled by powers of two first, since
 // typical values (P ~ 1/S, dS smaller still) sit in or below f16's subnormal range: P by 2^15
-// (P <= 1), dS by the sigma below, both undone on the fp32 accumulators.  With
-// A = max_q |dO_q| and B = max_k |V_k| (Euclidean norms over one head's channels),
-// |dP - delta| <= 2 A B, so sigma = 2^floor(14 - log2(2 A B)) keeps every |dS| below 2^15.
+// (P <= 1), dS by a sigma, both undone on the fp32 accumulators.  With A the Euclidean norm of a row of dO
+// over one head's channels and B = max_k |V_k|, |dP - delta| <= 2 A B in that row, so
+// sigma = 2^floor(14 - log2(2 A B)) keeps its |dS| below 2^15.  The query pass, whose accumulator rows
+// are queries, takes each row's own A: a row 2^24 times smaller than another keeps its 11 bits.  The key pass
+// sums over the queries and takes the largest A of the head: each dS there is held to within 2^-38 of the
+// head's largest 2 A B (half of f16's last step, 2^-25, over 2^13) or to 11 bits, whichever is coarser.
 #include "common.cuh"
 #include "pipeline.cuh"
 #include "train.h"
@@ -54,12 +57,13 @@ struct DqShape {
 __host__ __device__ inline int blocks_of(int seq) { return (seq + T - 1) / T; }
 
 // Per (b, h), nblk = the blocks of 128 rows and one more (blocks of any R <= 128 rows end inside it):
-// nlse2 / ndelta [B, H, nblk * 128], -log2(e) lse and -delta; norms2 [B, H, nblk]: the block's max
-// |dO_q|^2 and max |V_k|^2 (f16 only); tails: zero-padded copies [3: q, k, dO][B, 128, H hd] of the
+// nlse2 / ndelta / rows2 [B, H, nblk * 128], -log2(e) lse, -delta and (f16 only) |dO_q|^2; norms2
+// [B, H, nblk]: the block's max |dO_q|^2 and max |V_k|^2 (f16 only); tails: zero-padded copies [3: q, k, dO][B, 128, H hd] of the
 // block in which the tokens end.
 struct Workspace {
   float* nlse2;
   float* ndelta;
+  float* rows2;
   float2* norms2;
   uint16_t* tails;
   size_t bytes;
@@ -75,9 +79,10 @@ static Workspace carve(void* base, int batch, int seq, int n_heads, int head_dim
   uint8_t* b = static_cast<uint8_t*>(base);
   w.nlse2 = reinterpret_cast<float*>(b);
   w.ndelta = reinterpret_cast<float*>(b + vec);
-  w.norms2 = reinterpret_cast<float2*>(b + 2 * vec);
-  w.tails = reinterpret_cast<uint16_t*>(b + 2 * vec + nrm);
-  w.bytes = 2 * vec + nrm + tail;
+  w.rows2 = reinterpret_cast<float*>(b + 2 * vec);
+  w.norms2 = reinterpret_cast<float2*>(b + 3 * vec);
+  w.tails = reinterpret_cast<uint16_t*>(b + 3 * vec + nrm);
+  w.bytes = 3 * vec + nrm + tail;
   return w;
 }
 
@@ -92,7 +97,7 @@ struct PrepArgs {
   int64_t ldq, ldk, ldv;
   const float* lse;
   const int32_t* key_lens;
-  float *nlse2, *ndelta;
+  float *nlse2, *ndelta, *rows2;
   float2* norms2;
   uint16_t* tails;
   int batch, seq, n_heads;
@@ -120,6 +125,7 @@ __global__ void __launch_bounds__(PREP_THREADS) bwd_prep_kernel(const PrepArgs a
   const int64_t bh = static_cast<int64_t>(b) * a.n_heads + h;
   float* nlse2 = a.nlse2 + (bh * nblk + blk) * T;
   float* ndelta = a.ndelta + (bh * nblk + blk) * T;
+  float* rows2 = a.rows2 + (bh * nblk + blk) * T;
   float mdo = 0.f, mv = 0.f;
   // rows that take no part read the element's first row (a block past the tokens reads none)
   constexpr int CHUNK = 2;
@@ -172,6 +178,7 @@ __global__ void __launch_bounds__(PREP_THREADS) bwd_prep_kernel(const PrepArgs a
       if (c == 0) {
         // rows that take no part: exp2(s - inf) = 0
         ndelta[r] = -dot;
+        if constexpr (F == FMT_F16) rows2[r] = sdo;
         nlse2[r] = row < n ? (F == FMT_F16 ? P_SHIFT : 0.f) - a.lse[bh * a.seq + row] * LOG2E : -INFINITY;
       }
     }
@@ -215,12 +222,8 @@ __global__ void __launch_bounds__(PREP_THREADS) bwd_prep_kernel(const PrepArgs a
   }
 }
 
-// log2 of the factor dS is multiplied by before its rounding to f16 (0 in bf16, whose exponent
-// range is fp32's): 14 - log2(2 A B) rounded down, from the per-block maxima.  Norms of zero, or
-// ones that are not finite, leave it at 0.  Every lane of a warp calls it.
-template <int F>
-__device__ __forceinline__ float ds_shift(const float2* norms2, int nblk) {
-  if constexpr (F != FMT_F16) return 0.f;
+// The head's max |dO_q|^2 and max |V_k|^2 from the per-block maxima.  Every lane of a warp calls it.
+__device__ __forceinline__ float2 max_norms(const float2* norms2, int nblk) {
   float a = 0.f, b = 0.f;
   for (int i = static_cast<int>(lane_id()); i < nblk; i += 32) {
     const float2 x = norms2[i];
@@ -231,8 +234,15 @@ __device__ __forceinline__ float ds_shift(const float2* norms2, int nblk) {
     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
   }
-  // 2 A B = 2 sqrt(a b); the sum of logs cannot overflow
-  const float l = 1.f + 0.5f * (log2f(a) + log2f(b));
+  return make_float2(a, b);
+}
+
+// log2 of the factor dS is multiplied by before its rounding to f16 (bf16, whose exponent range is
+// fp32's, needs none): 14 - log2(2 A B) rounded down, from A^2 and B^2.  Norms of zero, or ones that are not
+// finite, leave it at 0.
+__device__ __forceinline__ float ds_shift(float a2, float b2) {
+  // 2 A B = 2 sqrt(a2 b2); the sum of logs cannot overflow
+  const float l = 1.f + 0.5f * (log2f(a2) + log2f(b2));
   return l > -100.f && l < 100.f ? floorf(14.f - l) : 0.f;
 }
 
@@ -632,7 +642,7 @@ __device__ __forceinline__ void drain_loads(const Pipe<L, HD>& p, int n_at, int 
 }
 
 struct BwdArgs {
-  const float *nlse2, *ndelta;
+  const float *nlse2, *ndelta, *rows2;
   const float2* norms2;
   OutRows dq, dk, dv;
   const int32_t* key_lens;
@@ -793,7 +803,8 @@ __device__ __forceinline__ void dkv_pass(const Pipe<DkvLayout<HD>, HD>& p, uint8
     auto shift_of = [&](int i) {
       if (F != FMT_F16 || i >= items.live) return 0.f;
       const Item it = items.at(i);
-      return ds_shift<F>(norms2 + it.bh * nblk, blocks_of(it.n));
+      const float2 m = max_norms(norms2 + it.bh * nblk, blocks_of(it.n));
+      return ds_shift(m.x, m.y);
     };
     bool ok = true;
     int u = 0, ui = 0;
@@ -896,7 +907,6 @@ __device__ __forceinline__ void dq_pass(const Pipe<DqLayout<HD>, HD>& p, uint8_t
   // two steps cost 861 us where one, spilling, cost 883 (4608 tokens x 32 heads, bf16)
   constexpr int STEP = HD == 128 ? 16 : COLS;
   const float *nlse2 = a.nlse2, *ndelta = a.ndelta;
-  const float2* norms2 = a.norms2;
   const OutRows dq = a.dq;
   const int seq = a.seq;
   const int warp = static_cast<int>(warp_id());
@@ -1017,7 +1027,7 @@ __device__ __forceinline__ void dq_pass(const Pipe<DqLayout<HD>, HD>& p, uint8_t
       const int64_t at = it.bh * nblk * T + it.tt * 2 * T + rank * T + r;
       s.nl = nlse2[at];
       s.nd = ndelta[at];
-      s.shift = ds_shift<F>(norms2 + it.bh * nblk, blocks_of(it.n));
+      if constexpr (F == FMT_F16) s.shift = ds_shift(a.rows2[at], max_norms(a.norms2 + it.bh * nblk, blocks_of(it.n)).y);
       return s;
     };
     bool ok = true;
@@ -1249,15 +1259,15 @@ static cudaError_t launch_hd(Rows q, Rows k, Rows v, const void* out, const void
   if (e != cudaSuccess) return e;
   const PrepArgs pa{static_cast<const uint16_t*>(q.p), static_cast<const uint16_t*>(k.p),
                     static_cast<const uint16_t*>(v.p), static_cast<const uint16_t*>(out),
-                    static_cast<const uint16_t*>(dout), q.ld, k.ld, v.ld, lse, key_lens, w.nlse2, w.ndelta, w.norms2,
-                    w.tails, batch, seq, n_heads};
+                    static_cast<const uint16_t*>(dout), q.ld, k.ld, v.ld, lse, key_lens, w.nlse2, w.ndelta, w.rows2,
+                    w.norms2, w.tails, batch, seq, n_heads};
   e = launch_pdl(bwd_prep_kernel<HD, F>, dim3(nblk, n_heads, batch), dim3(PREP_THREADS), 0, s, pa);
   if (e != cudaSuccess) return e;
   int sms = 0, dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     sms = 148;
   auto view = [](Rows r) { return OutRows{static_cast<uint16_t*>(const_cast<void*>(r.p)), r.ld}; };
-  const BwdArgs args{w.nlse2, w.ndelta, w.norms2, view(dq), view(dk), view(dv), key_lens, batch, seq, n_heads};
+  const BwdArgs args{w.nlse2, w.ndelta, w.rows2, w.norms2, view(dq), view(dk), view(dv), key_lens, batch, seq, n_heads};
   const int64_t items = static_cast<int64_t>((seq + 2 * T - 1) / (2 * T)) * n_heads * batch, pairs = sms / 2;
   const dim3 grid(2u * static_cast<unsigned>(2 * items < pairs ? 2 * items : pairs));
   return launch_pdl(bwd_kernel<HD, F>, grid, dim3(Shared<HD>::THREADS), Shared<HD>::SMEM, s, maps, args, g);
