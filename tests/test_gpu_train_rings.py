@@ -6,7 +6,7 @@ import torch
 import train_ref as R
 from joint_attention_block_b200 import ops
 from test_gpu_train import FMTS, _clean_errors, qk_backward_case, qkv_case  # noqa: F401
-from train_ref import nan_like, run_backward, run_forward, ws
+from train_ref import nan_like, run_backward, run_forward, within, ws
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,35 @@ def test_attention_gradients_in_a_row_in_one_workspace(S, H, hd, fmt):
     torch.cuda.synchronize()
     for i, (g, ref) in enumerate(zip(got, refs)):
         assert torch.equal(g, ref), i
+
+
+@FMTS
+@pytest.mark.parametrize("padded", [False, True], ids=["full", "padded"])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_gradient_of_many_long_items(hd, padded, fmt):
+    """Nearly three items of two tiles and four to six blocks for each of the 74 CTA pairs and pass, so that rings and
+    accumulators run on from item to item; heads and elements of very different size, so that one item's scale of
+    dS (f16) is wrong for the next; in the padded batch the last items of a pair are only zeroed."""
+    B, S, H = 26, 420, 4
+    d = H * hd
+    q, k, v, do = (R.heads(t, H).clone() for t in qkv_case(B, S, H, hd, fmt, 500 + hd))
+    size = torch.arange(B * H, device="cuda").view(B, H, 1, 1)
+    v = v * 2.0 ** ((size * 5) % 11 - 5)
+    do = do * 2.0 ** ((size * 7) % 17 - 8)
+    q, k, v, do = (R.flat(t).to(R.DT[fmt]) for t in (q, k, v, do))
+    lens = [(0, 420, 257, 416, 400, 1, 385)[b % 7] for b in range(B)] if padded else [S] * B
+    kl = torch.tensor(lens, dtype=torch.int32, device="cuda") if padded else None
+    out, lse = run_forward(q, k, v, H, hd, fmt, kl)
+    g = run_backward(q, k, v, out, do, lse, H, hd, fmt, kl)
+    for b, n in enumerate(lens):
+        assert not g[b, n:].any()
+        if n == 0:
+            continue
+        q1, k1, v1, o1, do1 = (t[b:b + 1, :n] for t in (q, k, v, out, do))
+        ref, ref_lse, tol, tol_lse = R.attention_bounds(*(R.heads(t, H) for t in (q1, k1, v1)), fmt)
+        within(R.heads(o1, H), ref, tol, f"out of element {b}")
+        within(lse[b:b + 1, :, :n], ref_lse, tol_lse, f"lse of element {b}")
+        refs, tols = R.attention_grad_bounds(*(R.heads(t, H) for t in (q1, k1, v1, o1, do1)),
+                                             lse[b:b + 1, :, :n].double(), fmt)
+        for i, name in enumerate(("dq", "dk", "dv")):
+            within(R.heads(g[b:b + 1, :n, i * d:(i + 1) * d], H), refs[i], tols[i], f"{name} of element {b}")
