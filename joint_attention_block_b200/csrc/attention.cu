@@ -49,6 +49,7 @@
 // 1080 TFLOP/s; the tensor core is busy in 51 % of the cycles and the exponentials' unit about as much, as in
 // the other form), 16896 tokens 4.32 ms against 4.17.
 #include "common.cuh"
+#include "pipeline.cuh"
 #include "qk8.h"
 #include "train.h"
 
@@ -235,8 +236,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     bool ok = true;
     for (int i = pair; i < items && ok; i += pairs, ++ui) {
       const Item it = item(i);
-      if (ui > 0 && !mbar_wait(q_empty, static_cast<uint32_t>(ui - 1) & 1u, guard, abort_flag,
-                               where_code(ERR_TIMEOUT_ATTN_PRODUCER, rank, 0xFFFF))) {
+      if (ui > 0 && !mbar_wait_warp(q_empty, static_cast<uint32_t>(ui - 1) & 1u, guard, abort_flag,
+                                    where_code(ERR_TIMEOUT_ATTN_PRODUCER, rank, 0xFFFF))) {
         ok = false;
         break;
       }
@@ -258,8 +259,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       for (int j = 0; j < it.nb; ++j) {
         const int st = issued % STAGES;
         const uint32_t rnd = static_cast<uint32_t>(issued / STAGES);
-        if (!mbar_wait(&kv_empty[st], (rnd & 1u) ^ 1u, guard, abort_flag,
-                       where_code(ERR_TIMEOUT_ATTN_PRODUCER, rank, issued))) {
+        if (!mbar_wait_warp(&kv_empty[st], (rnd & 1u) ^ 1u, guard, abort_flag,
+                            where_code(ERR_TIMEOUT_ATTN_PRODUCER, rank, issued))) {
           ok = false;
           break;
         }
@@ -303,7 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
   } else if (warp == 1) {
     // ---------------- MMA issuer (leader only)
     if (leader) {
-        // kind::f16 for 16-bit q, k; kind::f8f6f4 (type code 0: e4m3) for Q8
+      // kind::f16 for 16-bit q, k; kind::f8f6f4 (type code 0: e4m3) for Q8
       constexpr uint32_t idesc_s = idesc_f16kind(2 * BQ, BKV, Q8 ? true : kF16, false, false);
       constexpr uint32_t idesc_o = idesc_f16kind(2 * BQ, HD, kF16, false, true);
       // g: key block index over all work items (the ring slot and the barrier phases); j: the
@@ -338,6 +339,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           mma_f16kind_ts_pair(tmem + 256 * t + 128, tmem + 256 * t + 8 * kk, bd, idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
         }
       };
+      // one lane issues: an elected one at head dim 128 in 16 bits (4608 x 32 heads 302 us, with the log-sum-exps
+      // 301; lane 0 305 and 312), lane 0 at head dim 64 (4608 x 64 heads 526; elected 539) and for e4m3 (276; 284)
+      const bool one = HD == 128 && !Q8 ? elect_one() : lane == 0;
       bool ok = true;
       int gb = 0;  // key blocks of the items before this one
       int ui = 0;
@@ -346,13 +350,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int nb = it.nb;
         // S_A(0), S_B(0) overwrite S (and P) of the previous item only after its P V MMAs,
         // issued before them, have read P
-        ok = mbar_wait(q_full, static_cast<uint32_t>(ui) & 1u, guard, abort_flag,
-                       where_code(ERR_TIMEOUT_ATTN_MMA, rank, 0)) &&
-             mbar_wait(&k_full[gb % STAGES], static_cast<uint32_t>(gb / STAGES) & 1u, guard, abort_flag,
-                       where_code(ERR_TIMEOUT_ATTN_MMA, rank, gb));
+        ok = mbar_wait_warp(q_full, static_cast<uint32_t>(ui) & 1u, guard, abort_flag,
+                            where_code(ERR_TIMEOUT_ATTN_MMA, rank, 0)) &&
+             mbar_wait_warp(&k_full[gb % STAGES], static_cast<uint32_t>(gb / STAGES) & 1u, guard, abort_flag,
+                            where_code(ERR_TIMEOUT_ATTN_MMA, rank, gb));
         if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
+        if (one) {
           issue_s(0, gb);
           issue_s(1, gb);
           if (nb == 1) mma_commit_pair(q_empty, 0x3);  // the item's last S MMAs are issued: Q free after them
@@ -365,28 +369,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const bool next = j + 1 < nb;
           // the first P V of an item overwrites O_t: both CTAs' epilogues of the previous item
           // must have read it
-          ok = mbar_wait(&v_full[st], static_cast<uint32_t>(g / STAGES) & 1u, guard, abort_flag,
-                         where_code(ERR_TIMEOUT_ATTN_MMA, 1, g)) &&
-               mbar_wait(&p_full[0], par, guard, abort_flag, where_code(ERR_TIMEOUT_ATTN_MMA, 2, g)) &&
-               (!next || mbar_wait(&k_full[(g + 1) % STAGES], static_cast<uint32_t>((g + 1) / STAGES) & 1u, guard,
-                                   abort_flag, where_code(ERR_TIMEOUT_ATTN_MMA, 3, g))) &&
-               (j > 0 || ui == 0 ||
+          // after a wait that gave up the warp goes on to the end of the block (on whatever it finds; the error
+          // word is set) and leaves by the vote there, so that it cannot split
+          ok &= mbar_wait(&v_full[st], static_cast<uint32_t>(g / STAGES) & 1u, guard, abort_flag,
+                          where_code(ERR_TIMEOUT_ATTN_MMA, 1, g));
+          ok &= mbar_wait(&p_full[0], par, guard, abort_flag, where_code(ERR_TIMEOUT_ATTN_MMA, 2, g));
+          ok &= !next || mbar_wait(&k_full[(g + 1) % STAGES], static_cast<uint32_t>((g + 1) / STAGES) & 1u, guard,
+                                   abort_flag, where_code(ERR_TIMEOUT_ATTN_MMA, 3, g));
+          ok &= j > 0 || ui == 0 ||
                 mbar_wait(&o_empty[0], static_cast<uint32_t>(ui - 1) & 1u, guard, abort_flag,
-                          where_code(ERR_TIMEOUT_ATTN_MMA, 5, g)));
-          if (!ok) break;
+                          where_code(ERR_TIMEOUT_ATTN_MMA, 5, g));
           tc_fence_after();
-          if (lane == 0) {
+          if (one) {
             issue_pv(0, g, j);
             if (next) issue_s(0, g + 1);  // overwrites P_A only after P V_A has read it (in-order issue)
           }
           __syncwarp();
-          ok = mbar_wait(&p_full[1], par, guard, abort_flag, where_code(ERR_TIMEOUT_ATTN_MMA, 4, g)) &&
-               (j > 0 || ui == 0 ||
+          ok &= mbar_wait(&p_full[1], par, guard, abort_flag, where_code(ERR_TIMEOUT_ATTN_MMA, 4, g));
+          ok &= j > 0 || ui == 0 ||
                 mbar_wait(&o_empty[1], static_cast<uint32_t>(ui - 1) & 1u, guard, abort_flag,
-                          where_code(ERR_TIMEOUT_ATTN_MMA, 6, g)));
-          if (!ok) break;
+                          where_code(ERR_TIMEOUT_ATTN_MMA, 6, g));
           tc_fence_after();
-          if (lane == 0) {
+          if (one) {
             issue_pv(1, g, j);
             mma_commit_pair(&kv_empty[st], 0x3);  // K_g and V_g fully consumed by both tiles
             if (next) {
@@ -394,13 +398,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
               if (j + 2 == nb) mma_commit_pair(q_empty, 0x3);  // the item's last S MMAs are issued
             }
           }
-          __syncwarp();
+          ok = __all_sync(0xffffffffu, ok);
         }
-        if (ok && lane == 0) mma_commit_pair(o_full, 0x3);  // this item's O final
+        if (ok && one) mma_commit_pair(o_full, 0x3);  // this item's O final
         __syncwarp();
         gb += nb;
       }
-      if (lane == 0) mma_commit_pair(drain_bar, 0x3);  // all MMAs retired before either CTA frees TMEM
+      if (one) mma_commit_pair(drain_bar, 0x3);  // all MMAs retired before either CTA frees TMEM
       __syncwarp();
     }
     mbar_wait(drain_bar, 0u, guard, abort_flag, where_code(ERR_TIMEOUT_ATTN_DRAIN, rank, 1), true);
@@ -416,9 +420,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // (Q8: times the two e4m3 scales, S being accumulated from the codes)
     constexpr float c_log2_16 = 1.4426950408889634f / (HD == 128 ? 11.313708498984761f : 8.0f);
     const float c_log2 = Q8 ? c_log2_16 * (qk_scale[0] * qk_scale[1]) : c_log2_16;
-    bool ok = true;
     uint32_t sph = 0u;  // phase parity of s_full[t]: one phase per key block, all items
-    for (int ui = 0; pair + ui * pairs < items && ok; ++ui) {
+    for (int ui = 0; pair + ui * pairs < items; ++ui) {
     int nkv, nb;
     {
       const Item it = item(pair + ui * pairs);
@@ -428,10 +431,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     float m_used = -INFINITY;
     float l = 0.f;
     for (int j = 0; j < nb; ++j) {
-      if (!mbar_wait(&s_full[t], sph, guard, abort_flag, where_code(ERR_TIMEOUT_ATTN_SOFTMAX, rank * 2 + t, j))) {
-        ok = false;
-        break;
-      }
+      // a wait that gave up has set the error word and the later ones give up soon: the lanes go on together, on
+      // whatever they find, to the item's last wait, whose verdict is the whole warp's (a flag carried through
+      // the block, or a vote at each, cost 3 %)
+      mbar_wait(&s_full[t], sph, guard, abort_flag, where_code(ERR_TIMEOUT_ATTN_SOFTMAX, rank * 2 + t, j));
       sph ^= 1u;
       tc_fence_after();
       const int valid = nkv - j * BKV;  // keys beyond this element's key count are masked
@@ -526,7 +529,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&p_full[t]), 0));
     }
-    if (!ok) break;
     if constexpr (LSE) {  // while the last P V runs; m_used is in log2 units of the scaled logits
       const Item it = item(pair + ui * pairs);
       const int row = it.q0 + 2 * BQ * t + r;
@@ -534,11 +536,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         lse[(static_cast<size_t>(it.b) * n_heads + it.head) * seq + row] =
             row < it.live ? (m_used + log2f(l)) * 0.6931471805599453f : 0.f;
     }
-    if (!mbar_wait(o_full, static_cast<uint32_t>(ui) & 1u, guard, abort_flag,
-                   where_code(ERR_TIMEOUT_ATTN_SOFTMAX, 4 + rank, t))) {
-      ok = false;
+    if (!mbar_wait_warp(o_full, static_cast<uint32_t>(ui) & 1u, guard, abort_flag,
+                        where_code(ERR_TIMEOUT_ATTN_SOFTMAX, 4 + rank, t)))
       break;
-    }
     {
       tc_fence_after();
       const Item it = item(pair + ui * pairs);
