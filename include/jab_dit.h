@@ -311,7 +311,11 @@ DIT_API int dit_joint_attention(const void* qkv, void* out, int fmt, int batch, 
  *   dit_joint_attention_backward  gradients of the rotated q and k, and of v
  *   dit_qknorm_mrope_backward   gradients of the raw q and k, and of the two gains
  *   dit_rmsnorm_rows_backward   gradient through the pre-norm, the residual's added, and of its gain
- * (the products with the frozen weights are dit_gemm_w8a16 on transposed codes).
+ * The gradient of a product with a frozen weight, dx = dy W for y = x W^T, is dit_gemm_w8a16 on the
+ * transposed codes [K, N].  The weight's scales, one per row of W, lie on that product's contraction axis and so go
+ * onto dy: with m the largest of them, pass dy * (scale / m), rounded to 16 bits, as the operand and m as the scale of
+ * each of the K output channels.  (dy * scale itself, with scales of amax / 448, would lie below F16's normal
+ * range: gradients of 1e-3 would keep a few bits and of 1e-4 hardly one.)
  *
  * Row views: a pointer with a leading dimension ld (elements) is a 16-bit [batch, seq, cols] view
  * whose rows are ld apart and whose batch elements are seq * ld apart; ld >= cols, ld % 8 == 0,
