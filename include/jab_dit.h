@@ -398,7 +398,8 @@ DIT_API size_t dit_rmsnorm_rows_backward_workspace_bytes(int64_t rows, int64_t c
  * F16 or F32); dres: optional gradient that reaches x past the norm (the residual), in dx_fmt, NULL
  * for none; dx: [rows, cols] in dx_fmt (BF16, F16 or F32), may be dres itself; dg: fp32 [cols],
  * overwritten (zeros for rows = 0).  fp32 math.
- * Errors: INVALID_ARG (cols % 8, dx aliasing x or dy), UNSUPPORTED (cols > 8192), WORKSPACE. */
+ * Errors: INVALID_ARG (cols % 8, dx aliasing x or dy; x, g, dy, dres or dx not 16-byte aligned, dg not
+ * 4-byte aligned), UNSUPPORTED (cols > 8192), WORKSPACE. */
 DIT_API int dit_rmsnorm_rows_backward(const void* x, int x_fmt, const void* g, const void* dy, int dy_fmt,
                                       const void* dres, void* dx, int dx_fmt, float* dg, int64_t rows, int64_t cols,
                                       float eps, void* workspace, size_t ws_bytes, void* stream);

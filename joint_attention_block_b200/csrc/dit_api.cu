@@ -876,7 +876,7 @@ int dit_rmsnorm_rows_backward(const void* x, int x_fmt, const void* g, const voi
   if ((x_fmt != FMT_BF16 && x_fmt != FMT_F32) || dy_fmt < FMT_BF16 || dy_fmt > FMT_F32 || dx_fmt < FMT_BF16 ||
       dx_fmt > FMT_F32)
     return DIT_ERR_INVALID_ARG;
-  if (dg == nullptr || !aligned16(dg)) return DIT_ERR_INVALID_ARG;
+  if (dg == nullptr || (reinterpret_cast<uintptr_t>(dg) & 3u) != 0) return DIT_ERR_INVALID_ARG;
   if (rows == 0) return from_cuda(cudaMemsetAsync(dg, 0, static_cast<size_t>(cols) * 4, as_stream(stream)));
   if (x == nullptr || g == nullptr || dy == nullptr || dx == nullptr || dx == x || dx == dy) return DIT_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(g) || !aligned16(dy) || !aligned16(dres) || !aligned16(dx)) return DIT_ERR_INVALID_ARG;

@@ -92,6 +92,15 @@ def test_rmsnorm_backward_refusals(lib):
     assert lib.dit_rmsnorm_rows_backward_workspace_bytes(4, 12) == 0
 
 
+def test_rmsnorm_backward_takes_any_slice_of_a_gradient_buffer(lib):
+    """dg is written a float at a time: 4-byte alignment is enough (the workspace is what is refused here)."""
+    def call(dg):
+        return lib.dit_rmsnorm_rows_backward(1024, 0, 2048, 4096, 0, None, 8192, 0, dg, 4, 64, 1e-6, None, 0, None)
+
+    assert call(12288) == call(12292) == call(12296) == call(12300) == WORKSPACE
+    assert call(12290) == call(12289) == INVALID
+
+
 def test_workspace_sizes(lib):
     # one zero-padded block of 128 rows per element
     assert lib.dit_joint_attention_lse_workspace_bytes(2, 1000, 4, 64) == 2 * 128 * 4 * 64 * 2
