@@ -335,7 +335,8 @@ DIT_API int dit_joint_attention(const void* qkv, void* out, int fmt, int batch, 
  *   positions; padding rows are computed like any row, at (0, 0, 0)).  Not together with pos.
  * key_lens: optional DEVICE int32 [batch], receives each element's token count (L_b + grid_h *
  *   grid_w, or S without text_lens).
- * Other arguments and errors as dit_qknorm_mrope; INVALID_ARG for qk == qkv. */
+ * Other arguments and errors as dit_qknorm_mrope; INVALID_ARG for qk == qkv and for key_lens over
+ * text_lens (the counts are written while the lengths are read). */
 DIT_API int dit_qknorm_mrope_out(const void* qkv, void* qk, int fmt, int batch, int n_text, int grid_h, int grid_w,
                                  int t_img, const int32_t* pos, const int32_t* text_lens, int32_t* key_lens,
                                  const dit_block_config* cfg, const void* g_q, const void* g_k, void* stream);

@@ -736,6 +736,12 @@ bool attn_shape_ok(int batch, int seq, int n_heads, int head_dim) {
   return tokens < (1ll << 31) / 16 && blocks < (1ll << 31) && static_cast<int64_t>(n_heads) * head_dim < (1ll << 24);
 }
 
+// [a, a + n) and [b, b + n) share a byte
+bool overlap(const void* a, const void* b, size_t n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + n && y < x + n;
+}
+
 bool rows_ok(const void* p, int64_t ld, int64_t cols) {
   return p != nullptr && aligned16(p) && ld >= cols && ld % 8 == 0 && ld < (1ll << 31);
 }
@@ -759,6 +765,9 @@ int dit_qknorm_mrope_out(const void* qkv, void* qk, int fmt, int batch, int n_te
     return DIT_ERR_INVALID_ARG;
   if (fmt != FMT_BF16 && fmt != FMT_F16) return DIT_ERR_INVALID_ARG;
   if (qkv == qk || (pos != nullptr && text_lens != nullptr)) return DIT_ERR_INVALID_ARG;
+  // one CTA writes an element's count while the others still read its length
+  if (text_lens != nullptr && key_lens != nullptr && overlap(text_lens, key_lens, static_cast<size_t>(batch) * 4))
+    return DIT_ERR_INVALID_ARG;
   if (!aligned16(qkv) || !aligned16(qk) || !aligned16(g_q) || !aligned16(g_k)) return DIT_ERR_INVALID_ARG;
   cudaStream_t s = as_stream(stream);
   prof_mark(s, DIT_KERNEL_QKNORM_MROPE);

@@ -92,6 +92,15 @@ def test_rmsnorm_backward_refusals(lib):
     assert lib.dit_rmsnorm_rows_backward_workspace_bytes(4, 12) == 0
 
 
+def test_counts_are_not_written_over_the_lengths(lib, cfg):
+    """key_lens inside text_lens would be written by one CTA while the others read it."""
+    def call(lens, counts, batch=2):
+        return lib.dit_qknorm_mrope_out(1024, 4096, 0, batch, 16, 8, 8, -1, None, lens, counts, ctypes.byref(cfg), 16, 32,
+                                        None)
+
+    assert call(512, 512) == call(512, 516) == call(516, 512) == call(512, 524, batch=4) == INVALID
+
+
 def test_rmsnorm_backward_takes_any_slice_of_a_gradient_buffer(lib):
     """dg is written a float at a time: 4-byte alignment is enough (the workspace is what is refused here)."""
     def call(dg):
