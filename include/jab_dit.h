@@ -326,6 +326,7 @@ DIT_API int dit_joint_attention(const void* qkv, void* out, int fmt, int batch, 
  * leading rows of each element that take part, as queries and as keys.  The rows behind them are
  * never used, whatever they hold (NaN included); their outputs and gradients are written as zeros.
  * Results do not depend on the order in which CTAs run: equal inputs give equal bits.
+ * fp32 and int32 arrays of these calls are 4-byte aligned (INVALID_ARG).
  * Each call uses its workspace until its kernels have finished; calls that may overlap (other
  * streams, captured graphs) need workspaces of their own. */
 

@@ -111,6 +111,11 @@ using namespace jab;
 namespace {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// fp32 and int32 arrays (NULL counts as aligned)
+template <typename... P>
+inline bool aligned4(P... p) {
+  return ((... | reinterpret_cast<uintptr_t>(p)) & 3u) == 0;
+}
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
@@ -768,7 +773,8 @@ int dit_qknorm_mrope_out(const void* qkv, void* qk, int fmt, int batch, int n_te
   // one CTA writes an element's count while the others still read its length
   if (text_lens != nullptr && key_lens != nullptr && overlap(text_lens, key_lens, static_cast<size_t>(batch) * 4))
     return DIT_ERR_INVALID_ARG;
-  if (!aligned16(qkv) || !aligned16(qk) || !aligned16(g_q) || !aligned16(g_k)) return DIT_ERR_INVALID_ARG;
+  if (!aligned16(qkv) || !aligned16(qk) || !aligned16(g_q) || !aligned16(g_k) || !aligned4(pos, text_lens, key_lens))
+    return DIT_ERR_INVALID_ARG;
   cudaStream_t s = as_stream(stream);
   prof_mark(s, DIT_KERNEL_QKNORM_MROPE);
   const cudaError_t e = launch_qknorm_mrope_out(
@@ -799,7 +805,8 @@ int dit_qknorm_mrope_backward(const void* qkv, const void* dqk, int64_t ld_dqk, 
   if (!rows_ok(dqk, ld_dqk, cols) || !rows_ok(dx, ld_dx, cols) || dx == qkv || (dx == dqk && ld_dx != ld_dqk) ||
       (pos != nullptr && text_lens != nullptr))
     return DIT_ERR_INVALID_ARG;
-  if (!aligned16(qkv) || !aligned16(g_q) || !aligned16(g_k)) return DIT_ERR_INVALID_ARG;
+  if (!aligned16(qkv) || !aligned16(g_q) || !aligned16(g_k) || !aligned4(dg_q, dg_k, pos, text_lens))
+    return DIT_ERR_INVALID_ARG;
   const int S = n_text + grid_h * grid_w;
   if (!ws_ok(workspace, ws_bytes, dit_qknorm_mrope_backward_workspace_bytes(cfg, batch, S))) return DIT_ERR_WORKSPACE;
   KernelGuard g;
@@ -825,7 +832,7 @@ int dit_joint_attention_lse(const void* q, int64_t ld_q, const void* k, int64_t 
   const int64_t d = static_cast<int64_t>(n_heads) * head_dim;
   if (!rows_ok(q, ld_q, d) || !rows_ok(k, ld_k, d) || !rows_ok(v, ld_v, d) || !rows_ok(out, d, d) || lse == nullptr)
     return DIT_ERR_INVALID_ARG;
-  if (out == q || out == k || out == v) return DIT_ERR_INVALID_ARG;
+  if (out == q || out == k || out == v || !aligned4(lse, key_lens)) return DIT_ERR_INVALID_ARG;
   for (int64_t ld : {ld_q, ld_k, ld_v})
     if (!rows_mappable(seq, ld)) return DIT_ERR_UNSUPPORTED;
   if (key_lens != nullptr &&
@@ -858,7 +865,7 @@ int dit_joint_attention_backward(const void* q, int64_t ld_q, const void* k, int
   const void* ins[5] = {q, k, v, out, dout};
   for (const void* p : ins)
     if (p == dq || p == dk || p == dv) return DIT_ERR_INVALID_ARG;
-  if (dq == dk || dq == dv || dk == dv) return DIT_ERR_INVALID_ARG;
+  if (dq == dk || dq == dv || dk == dv || !aligned4(lse, key_lens)) return DIT_ERR_INVALID_ARG;
   for (int64_t ld : {ld_q, ld_k, ld_v, ld_dq, ld_dk, ld_dv})
     if (!rows_mappable(seq, ld)) return DIT_ERR_UNSUPPORTED;
   if (!ws_ok(workspace, ws_bytes, dit_joint_attention_backward_workspace_bytes(batch, seq, n_heads, head_dim)))
@@ -885,7 +892,7 @@ int dit_rmsnorm_rows_backward(const void* x, int x_fmt, const void* g, const voi
   if ((x_fmt != FMT_BF16 && x_fmt != FMT_F32) || dy_fmt < FMT_BF16 || dy_fmt > FMT_F32 || dx_fmt < FMT_BF16 ||
       dx_fmt > FMT_F32)
     return DIT_ERR_INVALID_ARG;
-  if (dg == nullptr || (reinterpret_cast<uintptr_t>(dg) & 3u) != 0) return DIT_ERR_INVALID_ARG;
+  if (dg == nullptr || !aligned4(dg)) return DIT_ERR_INVALID_ARG;
   if (rows == 0) return from_cuda(cudaMemsetAsync(dg, 0, static_cast<size_t>(cols) * 4, as_stream(stream)));
   if (x == nullptr || g == nullptr || dy == nullptr || dx == nullptr || dx == x || dx == dy) return DIT_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(g) || !aligned16(dy) || !aligned16(dres) || !aligned16(dx)) return DIT_ERR_INVALID_ARG;

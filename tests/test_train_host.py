@@ -92,6 +92,23 @@ def test_rmsnorm_backward_refusals(lib):
     assert lib.dit_rmsnorm_rows_backward_workspace_bytes(4, 12) == 0
 
 
+def test_misaligned_arrays_are_refused(lib, cfg):
+    """A float or int32 array off its 4 bytes would fault in the kernel."""
+    assert lse_call(lib, lse=16386) == lse_call(lib, lens=513, ws=WS, ws_bytes=1 << 30) == INVALID
+    assert backward_call(lib, lse=16385) == backward_call(lib, lens=514) == INVALID
+    c = ctypes.byref(cfg)
+
+    def out(pos=None, lens=None, counts=None):
+        return lib.dit_qknorm_mrope_out(1024, 4096, 0, 1, 16, 8, 8, -1, pos, lens, counts, c, 16, 32, None)
+
+    def back(dgq=64, dgk=1024, pos=None, lens=None):
+        return lib.dit_qknorm_mrope_backward(1024, 4096, 512, 8192, 512, dgq, dgk, 0, 1, 16, 8, 8, -1, pos, lens, c, 16, 32,
+                                             WS, 1 << 20, None)
+
+    assert out(pos=66) == out(lens=66) == out(counts=65) == INVALID
+    assert back(dgq=66) == back(dgk=1025) == back(pos=66) == back(lens=67) == INVALID
+
+
 def test_counts_are_not_written_over_the_lengths(lib, cfg):
     """key_lens inside text_lens would be written by one CTA while the others read it."""
     def call(lens, counts, batch=2):
