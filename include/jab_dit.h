@@ -326,6 +326,9 @@ DIT_API int dit_joint_attention(const void* qkv, void* out, int fmt, int batch, 
  * leading rows of each element that take part, as queries and as keys.  The rows behind them are
  * never used, whatever they hold (NaN included); their outputs and gradients are written as zeros.
  * Results do not depend on the order in which CTAs run: equal inputs give equal bits.
+ * Gradients do not saturate: beyond F16's range they are infinities, and an infinity or NaN in an incoming gradient
+ * reaches every gradient it enters, so that a loss scaler sees it (the forward forms saturate in F16 like the calls
+ * they belong to, dit_gemm_w8a16 with y_fmt F16 among them; with y_fmt F32 or BF16 it does not).
  * fp32 and int32 arrays of these calls are 4-byte aligned (INVALID_ARG).
  * Each call uses its workspace until its kernels have finished; calls that may overlap (other
  * streams, captured graphs) need workspaces of their own. */

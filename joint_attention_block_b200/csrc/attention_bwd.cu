@@ -376,7 +376,7 @@ __device__ __forceinline__ void store_box(const CUtensorMap* m, uint8_t* stage, 
     float o[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) o[k] = live ? __uint_as_float(raw[8 * q + k]) * f : 0.f;
-    store8<F>(stage + lane_id() * (2 * OUT), q, o);
+    store8<F, false>(stage + lane_id() * (2 * OUT), q, o);
   }
   fence_proxy_async_smem();
   __syncwarp();
@@ -839,7 +839,7 @@ __device__ __forceinline__ void dkv_pass(const Pipe<DkvLayout<HD>, HD>& p, uint8
           const float2 x = fma2(as_f2(raw + k), c2, *reinterpret_cast<const float2*>(vec + k));
           e[k] = ex2_approx(x.x);
           e[k + 1] = ex2_approx(x.y);
-          pk[k / 2] = pack2<F>(e[k], e[k + 1]);
+          pk[k / 2] = pack2<F, false>(e[k], e[k + 1]);
         }
         ok &= mbar_wait(p.p_empty, par ^ 1u, guard, p.abort_flag, where(2, u));  // dV(u - 1) has read P
         tc_fence_after();
@@ -856,7 +856,7 @@ __device__ __forceinline__ void dkv_pass(const Pipe<DkvLayout<HD>, HD>& p, uint8
           float2 y = mul2(add2(as_f2(raw + k), *reinterpret_cast<const float2*>(vec + R + k)),
                           make_float2(e[k], e[k + 1]));
           if constexpr (F == FMT_F16) y = mul2(y, make_float2(tau, tau));
-          pk[k / 2] = pack2<F>(y.x, y.y);
+          pk[k / 2] = pack2<F, false>(y.x, y.y);
         }
         ok &= mbar_wait(p.ds_empty, par ^ 1u, guard, p.abort_flag, where(4, u));  // dK(u - 1) has read dS
         tc_fence_after();
@@ -1083,7 +1083,7 @@ __device__ __forceinline__ void dq_pass(const Pipe<DqLayout<HD>, HD>& p, uint8_t
           for (int k = 0; k < STEP; k += 2) {
             const float2 v = as_f2(dp + k);
             const float2 y = mul2(F == FMT_F16 ? fma2(v, tau2, nd2) : add2(v, nd2), make_float2(e[c + k], e[c + k + 1]));
-            pk[(c + k) / 2] = pack2<F>(y.x, y.y);
+            pk[(c + k) / 2] = pack2<F, false>(y.x, y.y);
           }
         }
         ok &= mbar_wait(p.ds_empty, par ^ 1u, guard, p.abort_flag, where(8, u));  // dQ(u - 1) has read dS

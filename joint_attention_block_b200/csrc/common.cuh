@@ -77,9 +77,17 @@ JAB_DEVICE float f16_hi(uint32_t v) {
   return f;
 }
 
-template <int F>
+// pack_f16x2 without saturation, for gradients: beyond the range an infinity, and infinities stay, so that whoever
+// scales a loss sees them.
+JAB_DEVICE uint32_t pack_f16x2_inf(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int F, bool SATURATE = true>
 JAB_DEVICE uint32_t pack2(float lo, float hi) {
-  if constexpr (F == FMT_F16) return pack_f16x2(lo, hi);
+  if constexpr (F == FMT_F16) return SATURATE ? pack_f16x2(lo, hi) : pack_f16x2_inf(lo, hi);
   else return pack_bf16x2(lo, hi);
 }
 template <int F>
@@ -112,17 +120,17 @@ JAB_DEVICE void load8(const void* base, int64_t idx8, float (&v)[8]) {
 }
 
 // Store 8 consecutive values in format F.
-template <int F>
+template <int F, bool SATURATE = true>
 JAB_DEVICE void store8(void* base, int64_t idx8, const float (&v)[8]) {
   if constexpr (F == FMT_F32) {
     reinterpret_cast<float4*>(base)[2 * idx8] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4*>(base)[2 * idx8 + 1] = make_float4(v[4], v[5], v[6], v[7]);
   } else {
     uint4 o;
-    o.x = pack2<F>(v[0], v[1]);
-    o.y = pack2<F>(v[2], v[3]);
-    o.z = pack2<F>(v[4], v[5]);
-    o.w = pack2<F>(v[6], v[7]);
+    o.x = pack2<F, SATURATE>(v[0], v[1]);
+    o.y = pack2<F, SATURATE>(v[2], v[3]);
+    o.z = pack2<F, SATURATE>(v[4], v[5]);
+    o.w = pack2<F, SATURATE>(v[6], v[7]);
     reinterpret_cast<uint4*>(base)[idx8] = o;
   }
 }

@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(MAX_THREADS + 64, qk_ctas(MAX_THREADS))
       zb[k] = r * fmaf(-m, xb[k], zb[k] * gb[k]);
     }
     if (mine) {
-      store8<F>(out, 0, za);
-      store8<F>(out + half, 0, zb);
+      store8<F, false>(out, 0, za);
+      store8<F, false>(out + half, 0, zb);
     }
   };
 
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(256, row_ctas(V, XF == FMT_F32 || DF == FMT_F3
         acc[j][k] = fmaf(yv[j][k], xv[j][k] * r, acc[j][k]);
         e[j][k] = fmaf(r, fmaf(-m, xv[j][k], yv[j][k] * gv[k]), e[j][k]);
       }
-      if (lane + 32 * j < nv) store8<OF>(dx, row * nv + lane + 32 * j, e[j]);
+      if (lane + 32 * j < nv) store8<OF, false>(dx, row * nv + lane + 32 * j, e[j]);
     }
   }
 #pragma unroll
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(512, V == 1 ? 2 : 1)
         acc[j][k] = fmaf(yv[j][k], xv[j][k] * r, acc[j][k]);
         o[k] = fmaf(r, fmaf(-m, xv[j][k], yv[j][k] * gv[j][k]), e[k]);
       }
-      store8<OF>(dx, row * nv + i, o);
+      store8<OF, false>(dx, row * nv + i, o);
     }
   }
   if (threadIdx.x == 0) {  // never leave with copies in flight
