@@ -585,8 +585,7 @@ cudaError_t launch_hd(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
                       int seq, int n_heads, const int32_t* kv_len, const KernelGuard& g, cudaStream_t s,
                       const float* qk_scale = nullptr, const CUtensorMap* tvt = nullptr, float* lse = nullptr) {
   using L = Layout<HD, Q8>;
-  cudaError_t e =
-      cudaFuncSetAttribute(attention_kernel<HD, F, Q8, LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+  const cudaError_t e = allow_smem<attention_kernel<HD, F, Q8, LSE>>(L::SMEM);
   if (e != cudaSuccess) return e;
   // persistent: one CTA pair per SM pair at most, each walking work items (b, head, 512 queries)
   const long long items = static_cast<long long>(batch) * n_heads * ((seq + 4 * BQ - 1) / (4 * BQ));
@@ -660,9 +659,11 @@ cudaError_t launch_attention_q8(const uint8_t* q8, const uint8_t* k8, const floa
                         : attn::launch_hd<64, FMT_BF16, true>(tq, tk, tv, out, batch, seq, n_heads, kv_len, g, s, scale);
 }
 
-// One CTA per (row of the block, element); the element's last block, zero-padded.  A launch of 4 to 5 us
-// (4 elements x 1024 columns), all latency.
-__global__ void tail_rows_kernel(const uint16_t* __restrict__ src, int64_t ld, uint16_t* __restrict__ dst, int seq,
+// Zero-padded copies of the block of 128 rows in which each element's tokens end: for element b
+// with n = key_lens[b], n % 128 != 0 and n < seq, dst[b, r] = src[b, 128 (n / 128) + r] for the rows
+// before n and zero for the rest (dst [B, 128, cols], 16-bit; other elements are left as they are).  One CTA per
+// (row of the block, element).  A launch of 4 to 5 us (4 elements x 1024 columns), all latency.
+static __global__ void tail_rows_kernel(const uint16_t* __restrict__ src, int64_t ld, uint16_t* __restrict__ dst, int seq,
                                  int cols, const int32_t* __restrict__ key_lens) {
   pdl_wait_then_release();
   const int r = blockIdx.x, b = blockIdx.y;
@@ -674,8 +675,8 @@ __global__ void tail_rows_kernel(const uint16_t* __restrict__ src, int64_t ld, u
   for (int i = threadIdx.x; i < cols / 8; i += blockDim.x) to[i] = row < n ? from[i] : make_uint4(0u, 0u, 0u, 0u);
 }
 
-cudaError_t launch_tail_rows(Rows src, void* dst, int batch, int seq, int cols, const int32_t* key_lens,
-                             cudaStream_t s) {
+static cudaError_t launch_tail_rows(Rows src, void* dst, int batch, int seq, int cols, const int32_t* key_lens,
+                                    cudaStream_t s) {
   return launch_pdl(tail_rows_kernel, dim3(attn::BKV, static_cast<unsigned>(batch)), dim3(256), 0, s,
                     static_cast<const uint16_t*>(src.p), src.ld, static_cast<uint16_t*>(dst), seq, cols, key_lens);
 }

@@ -277,14 +277,6 @@ struct Layout {
   static_assert(OFF_OUT % 128 == 0 && (32 * OUT * 2) % 128 == 0, "staged pieces are TMA boxes");
 };
 
-// Global -> shared copy of a multiple of 16 bytes, both addresses 16-byte aligned.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // One own tile of 128 rows x HD; its completion is counted by the leader's barrier.
 template <class L, int HD>
 __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
@@ -385,11 +377,6 @@ __device__ __forceinline__ void store_box(const CUtensorMap* m, uint8_t* stage, 
     bulk_commit_group();
   }
   __syncwarp();
-}
-
-template <int N>
-__device__ __forceinline__ void bulk_wait_group() {
-  asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Zeros into this CTA's 128 rows from row0, those below seq, of one head; t: index among the N

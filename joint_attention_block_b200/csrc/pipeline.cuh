@@ -1,4 +1,4 @@
-// What the roles of a warp-specialised kernel share: one elected lane, and waits of whole warps.
+// What the roles of a warp-specialised kernel share: one elected lane, waits of whole warps, plain bulk copies.
 #pragma once
 
 #include "common.cuh"
@@ -21,6 +21,14 @@ JAB_DEVICE bool mbar_wait_warp(uint64_t* bar, uint32_t parity, const KernelGuard
                                uint32_t where) {
   const bool ok = mbar_wait(bar, parity, g, abort_flag, where);
   return __all_sync(0xffffffffu, ok);
+}
+
+// Global -> shared copy of a multiple of 16 bytes, both addresses 16-byte aligned.
+JAB_DEVICE void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
 }
 
 }  // namespace jab

@@ -44,12 +44,6 @@ cudaError_t launch_attention_bwd(Rows q, Rows k, Rows v, const void* out, const 
                                  Rows dk, Rows dv, int fmt, int batch, int seq, int n_heads, int head_dim,
                                  const int32_t* key_lens, void* workspace, const KernelGuard& g, cudaStream_t s);
 
-// Zero-padded copies of the block of 128 rows in which each element's tokens end: for element b
-// with n = key_lens[b], n % 128 != 0 and n < seq, dst[b, r] = src[b, 128 (n / 128) + r] for the rows
-// before n and zero for the rest (dst [B, 128, cols], 16-bit; other elements are left as they are).
-cudaError_t launch_tail_rows(Rows src, void* dst, int batch, int seq, int cols, const int32_t* key_lens,
-                             cudaStream_t s);
-
 // Per-head QK-RMSNorm + 3D M-RoPE of the raw q and k in the fused qkv buffer [B, S, 3d] into qk
 // [B, S, 2d]; key_lens (optional, [B]) receives each element's token count.
 cudaError_t launch_qknorm_mrope_out(const void* qkv, void* qk, int fmt, int batch, int seq, int n_heads, int head_dim,

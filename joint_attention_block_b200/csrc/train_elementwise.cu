@@ -5,6 +5,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "pipeline.cuh"
 #include "rope.cuh"
 #include "train.h"
 
@@ -41,13 +42,6 @@ static cudaError_t sum_rows(const float* part, int n, int64_t cols, float* dst0,
                             cudaStream_t s) {
   return launch_pdl(sum_rows_kernel, dim3(static_cast<unsigned>((cols + 31) / 32)), dim3(1024), 0, s, part, n, cols,
                     dst0, dst1, split);
-}
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
 }
 
 constexpr int MAX_STAGES = 8;
