@@ -111,7 +111,7 @@ struct PrepArgs {
 // rows' loads of 256 threads in flight the registers cost the large f16 call 36 us.
 constexpr int PREP_THREADS = 512;
 template <int HD, int F>
-__global__ void __launch_bounds__(PREP_THREADS) bwd_prep_kernel(const PrepArgs a) {
+__global__ void __launch_bounds__(PREP_THREADS, 3) bwd_prep_kernel(const PrepArgs a) {
   constexpr int LANES = HD / 8;
   constexpr int ROWS = PREP_THREADS / LANES;
   constexpr int PASSES = T / ROWS;
