@@ -437,7 +437,7 @@ struct Item {
 // The items in the order in which the pairs are dealt them, pair p taking p, p + pairs, ...  In a padded
 // batch the tiles that hold tokens come first, element by element, then the others, which are only zeroed:
 // with every element's tiles together the pairs' shares of the products came out uneven (1535, 1100, 1324
-// and 1023 tokens padded to 1535, 16 heads of 64: 148 us, now 139; 128 channels: 187, now 173).  Elements
+// and 1023 tokens padded to 1535, 16 heads of 64: 148 us against 139; 128 channels: 187 against 173).  Elements
 // of one tile stay together: they are uneven by a few blocks at most, and finding the place costs more
 // (512 elements of 80 or 10 tokens x 4 heads of 64: 191 us, in the other order 210).
 // Items are asked for in rising order, by whole warps: lane l holds the tiles of element chunk + l, summed
@@ -645,10 +645,10 @@ struct BwdArgs {
 // TMEM holds with a region of its own for each.  With 128 and P^T over S^T, dS^T over dP^T, S(j+1) waited for
 // dV(j) and dP(j+1) for dK(j): 3420 clocks a block against the products' 2048; with 96 and only
 // dS^T over dP^T 2030 against 1536.
-// 4608 queries and keys x 32 heads of 128 in f16: 517 us for the four products of this kernel (1350 TFLOP/s;
-// a large library product holds 1408 in a long run) at the 1.51 GHz that the power limit leaves, the tensor
-// core busy in 74 % of the cycles.  Bound by that limit and by the hand-over of S, P, dP and dS between the
-// tensor core and the elementwise warps.  64 heads of 64 in bf16: 658 us (1060 TFLOP/s).
+// As a launch of its own, 4608 queries and keys x 32 heads of 128 in f16: 517 us for the four products (1350
+// TFLOP/s; a large library product holds 1408 in a long run) at the 1.51 GHz that the power limit leaves, the
+// tensor core busy in 74 % of the cycles.  Bound by that limit and by the hand-over of S, P, dP and dS between
+// the tensor core and the elementwise warps.  64 heads of 64 in bf16: 658 us (1060 TFLOP/s).
 struct DkvMaps {
   CUtensorMap k, v, q_rows, q_cols, do_rows, do_cols, tq_rows, tq_cols, tdo_rows, tdo_cols, dk, dv;
 };
@@ -877,8 +877,9 @@ __device__ __forceinline__ void dkv_pass(const Pipe<DkvLayout<HD>, HD>& p, uint8
 
 // Own rows: queries; streamed: keys in blocks of 128.  S = Q K^T and dP = dO V^T, dS = P (dP - delta) as an
 // A operand in TMEM, dQ += dS K.  TMEM: S | dP | dS (64 columns) | dQ.  lse and delta are per thread.
-// 4608 x 32 heads of 128 in f16: 372 us for three products (1400 TFLOP/s) at 1.52 GHz, the tensor core busy
-// in 76 % of the cycles, the exponentials' unit in 57 %.  Bound as the key pass.  64 heads of 64: 505 us.
+// As a launch of its own with 95 registers a thread, 4608 x 32 heads of 128 in f16: 372 us for three products
+// (1400 TFLOP/s) at 1.52 GHz, the tensor core busy in 76 % of the cycles, the exponentials' unit in 57 %.  Bound as
+// the key pass.  64 heads of 64: 505 us.
 struct DqMaps {
   CUtensorMap q, dout, k_rows, k_cols, v_rows, tk_rows, tk_cols, dq;
 };
@@ -1141,7 +1142,8 @@ __device__ __noinline__ void dq_call(uint32_t tmem, const DqMaps& tm, const BwdA
 
 // One launch for both passes: nothing is read before the wait at its start, which orders everything either
 // pass reads after the preparation and all before it, and a pair that has no more key items goes on with its
-// query items at once.  Two launches, the second waiting for all of the first: 1100 tokens x 16 heads of 128 66 us
+// query items at once.  4608 x 32 heads of 128 in f16: 905 us, seven products at 1345 TFLOP/s and 1.54 GHz, the tensor
+// core busy in 72 % of the cycles.  Two launches, the second waiting for all of the first: 1100 tokens x 16 heads of 128 66 us
 // against 54, 80 tokens x 4 heads of 64 13.7 against 9.6, the padded batch of 16 heads of 64 151 against 146; 4608 x 32
 // heads of 128 852 against 861.
 template <int HD, int F>

@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(256, row_ctas(V, XF == FMT_F32 || DF == FMT_F3
 // Longer rows: a CTA per row at a time, V vectors of 8 per thread.  HBM-bound: x, dy and dres come
 // through a ring of bulk copies that keeps up to 200 KB in flight per SM.  With the sums' kernel, event-timed,
 // L2 cold: 4608 x 4096 fp32 rows with f16 dy 56 us (264 MB, 4.7 TB/s), bf16 41 us (151 MB, 3.6 TB/s), 16896 x 4096
-// bf16 109 us (5.1 TB/s), 4608 x 8192 bf16 58 us (5.2 TB/s).  From registers with one row fetched ahead the same took
+// bf16 111 us (5.0 TB/s), 4608 x 8192 bf16 58 us (5.2 TB/s).  From registers with one row fetched ahead the same took
 // 56, 44, 117 and 85 us.  A stage is free for its next row when the CTA has
 // met in the following row's reduction.
 template <int V, int XF, int DF, int OF>
