@@ -369,8 +369,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const bool next = j + 1 < nb;
           // the first P V of an item overwrites O_t: both CTAs' epilogues of the previous item
           // must have read it
-          // after a wait that gave up the warp goes on to the end of the block (on whatever it finds; the error
-          // word is set) and leaves by the vote there, so that it cannot split
+          // after a wait that gave up the warp goes on to the end of the block and leaves by the vote there, so that
+          // it cannot split; nothing more is issued or committed, so that no slot counts as free before its copies
+          // have landed
           ok &= mbar_wait(&v_full[st], static_cast<uint32_t>(g / STAGES) & 1u, guard, abort_flag,
                           where_code(ERR_TIMEOUT_ATTN_MMA, 1, g));
           ok &= mbar_wait(&p_full[0], par, guard, abort_flag, where_code(ERR_TIMEOUT_ATTN_MMA, 2, g));
@@ -380,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 mbar_wait(&o_empty[0], static_cast<uint32_t>(ui - 1) & 1u, guard, abort_flag,
                           where_code(ERR_TIMEOUT_ATTN_MMA, 5, g));
           tc_fence_after();
-          if (one) {
+          if (one && ok) {
             issue_pv(0, g, j);
             if (next) issue_s(0, g + 1);  // overwrites P_A only after P V_A has read it (in-order issue)
           }
@@ -390,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 mbar_wait(&o_empty[1], static_cast<uint32_t>(ui - 1) & 1u, guard, abort_flag,
                           where_code(ERR_TIMEOUT_ATTN_MMA, 6, g));
           tc_fence_after();
-          if (one) {
+          if (one && ok) {
             issue_pv(1, g, j);
             mma_commit_pair(&kv_empty[st], 0x3);  // K_g and V_g fully consumed by both tiles
             if (next) {

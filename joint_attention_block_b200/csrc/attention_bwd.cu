@@ -516,7 +516,9 @@ struct Items {
 //   the others        the elementwise step; thread = own row and COLS columns of the block
 // A wait gives up after a limit.  Its warp then goes on to the end of the block (on whatever it finds; the
 // error word is set) and leaves by a vote of its lanes: leaving lane by lane could split the warp, and a vote
-// at every wait cost 3 %.  Only the loads ask at once, since they may not arm a barrier that is in use.
+// at every wait cost 3 %.  Only the loads ask at once, since they may not arm a barrier that is in use; for the same
+// reason an issuing lane whose wait gave up issues and commits nothing more, so that no slot counts as free before its
+// copies have landed.
 // One lane of each issuing warp per pair runs the tensor cores of both SMs; with one warp for all
 // products its waits and commits took 1500 clocks a block, as long as the products.
 template <class L, int HD>
@@ -587,7 +589,7 @@ __device__ __forceinline__ void issue_s_dp(const Pipe<L, HD>& p, uint32_t t_s, u
       ok &= p.ra.wait_full(u, guard, p.abort_flag, where(1, u));
       ok &= u == 0 || mbar_wait(p.s_empty, prev, guard, p.abort_flag, where(2, u));
       tc_fence_after();
-      if (one) {
+      if (one && ok) {
         mma_rows<L, HD, F>(t_s, p.tile_a, slot);
         mma_commit_pair(p.s_full, 0x3);
         if (j + 1 == nb) mma_commit_pair(&p.at.empty[0], 0x3);
@@ -596,7 +598,7 @@ __device__ __forceinline__ void issue_s_dp(const Pipe<L, HD>& p, uint32_t t_s, u
       ok &= j > 0 || p.bt.wait_full(ui, guard, p.abort_flag, where(3, u));
       ok &= u == 0 || mbar_wait(p.dp_empty, prev, guard, p.abort_flag, where(4, u));
       tc_fence_after();
-      if (one) {
+      if (one && ok) {
         mma_rows<L, HD, F>(t_dp, p.tile_b, slot + L::CUT);
         mma_commit_pair(p.dp_full, 0x3);
         mma_commit_pair(&p.ra.empty[u % L::N], 0x3);
@@ -750,14 +752,14 @@ __device__ __forceinline__ void dkv_pass(const Pipe<DkvLayout<HD>, HD>& p, uint8
           ok &= p.rb.wait_full(u, guard, p.abort_flag, where(6, u));
           ok &= mbar_wait(p.p_full, par, guard, p.abort_flag, where(7, u));
           tc_fence_after();
-          if (one) {
+          if (one && ok) {
             mma_cols<L, HD, F>(tmem + C_DV, tmem + C_P, slot, j > 0);
             mma_commit_pair(p.p_empty, 0x3);
           }
           __syncwarp();
           ok &= mbar_wait(p.ds_full, par, guard, p.abort_flag, where(8, u));
           tc_fence_after();
-          if (one) {
+          if (one && ok) {
             mma_cols<L, HD, F>(tmem + C_DK, tmem + C_DS, slot + L::CUT, j > 0);
             mma_commit_pair(p.ds_empty, 0x3);
             mma_commit_pair(&p.rb.empty[u % N], 0x3);
@@ -781,10 +783,12 @@ __device__ __forceinline__ void dkv_pass(const Pipe<DkvLayout<HD>, HD>& p, uint8
     const float scale = HD == 128 ? 0.08838834764831845f : 0.125f;
     const float2 c2 = make_float2(scale * LOG2E, scale * LOG2E);
     auto where = [&](int k, int i) { return where_code(ERR_TIMEOUT_ABWD_SOFTMAX, k, i); };
+    bool ok = true;
+    // (a copy of row vectors may be on its way into a slot whose wait gave up: no arrive then)
     auto arrive = [&](uint64_t* bar) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(bar), 0));
+      if (lane == 0 && ok) mbar_arrive_remote(mapa_shared(smem_u32(bar), 0));
     };
     uint8_t* stage = smem + L::OFF_OUT + (warp - L::FIRST_EW) * 32 * L::OUT * 2;
     auto shift_of = [&](int i) {
@@ -793,7 +797,6 @@ __device__ __forceinline__ void dkv_pass(const Pipe<DkvLayout<HD>, HD>& p, uint8
       const float2 m = max_norms(norms2 + it.bh * nblk, blocks_of(it.n));
       return ds_shift(m.x, m.y);
     };
-    bool ok = true;
     int u = 0, ui = 0;
     float shift = shift_of(first);
     for (int i = first; i < items.total && ok; i += pairs) {
@@ -974,7 +977,7 @@ __device__ __forceinline__ void dq_pass(const Pipe<DqLayout<HD>, HD>& p, uint8_t
           ok &= p.rb.wait_full(u, guard, p.abort_flag, where(10, u));
           ok &= mbar_wait(p.ds_full, static_cast<uint32_t>(u) & 1u, guard, p.abort_flag, where(11, u));
           tc_fence_after();
-          if (one) {
+          if (one && ok) {
             mma_cols<L, HD, F>(tmem + C_DQ, tmem + C_DS, p.mem_b + (u % N) * L::SLOT_B, j > 0);
             mma_commit_pair(p.ds_empty, 0x3);
             mma_commit_pair(&p.rb.empty[u % N], 0x3);

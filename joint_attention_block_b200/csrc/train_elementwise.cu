@@ -225,12 +225,13 @@ __global__ void __launch_bounds__(MAX_THREADS + 64, qk_ctas(MAX_THREADS))
     }
     const int st = u % stages;
     // a wait that gave up has set the error word and every later one gives up soon; the warp's lanes go on
-    // together, since they meet in every token's reduction
-    mbar_wait(&full[st], static_cast<uint32_t>(u / stages) & 1u, guard, &abort_flag, where_code(ERR_TIMEOUT_QKBWD, 2, u));
+    // together, since they meet in every token's reduction, but do not free a slot whose copies may be on their way
+    const bool got = mbar_wait(&full[st], static_cast<uint32_t>(u / stages) & 1u, guard, &abort_flag,
+                               where_code(ERR_TIMEOUT_QKBWD, 2, u));
     const uint16_t* x = reinterpret_cast<const uint16_t*>(ring + st * 2 * row_bytes) + h * HD + 8 * c;
     one(x, x + d, out, s_cos[st], s_sin[st]);
     __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[st]);
+    if (lane == 0 && got) mbar_arrive(&empty[st]);
     ++u;
   }
   __syncthreads();  // every warp is done with the ring, and its copies have landed
