@@ -47,6 +47,7 @@
 #include <string.h>
 
 #include "common.cuh"
+#include "pipeline.cuh"
 
 namespace jab {
 namespace gemm {
@@ -199,8 +200,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       for (int kb = 0; kb < w.num_kb; ++kb) {
         const int s = g % RAW_STAGES;
         const uint32_t it = static_cast<uint32_t>(g / RAW_STAGES);
-        if (!mbar_wait(&raw_empty[s], (it & 1u) ^ 1u, guard, abort_flag,
-                       where_code(ERR_TIMEOUT_GEMM_PRODUCER, rank, g))) {
+        if (!mbar_wait_warp(&raw_empty[s], (it & 1u) ^ 1u, guard, abort_flag,
+                            where_code(ERR_TIMEOUT_GEMM_PRODUCER, rank, g))) {
           ok = false;
           break;
         }
@@ -236,6 +237,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     // ---------------- MMA issuer (leader only)
     if (leader) {
       constexpr uint32_t idesc = idesc_f16kind(BM, BN_MMA, F16, false, false);
+      // an elected lane: 4608 x 12288 x 4096 in f16 310 us (lane 0: 315), 512 x 4096 x 53248 in bf16 558 (624)
+      const bool one = elect_one();
       bool ok = true;
       int g = 0;
       for (int u = pair; u < p.units && ok; u += pairs) {
@@ -245,13 +248,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           const int c = g % CVT_STAGES;
           // the first stage of a unit also waits, through the converters, for both epilogues
           // of the previous unit to have read the accumulators
-          ok = mbar_wait(&x_full[s], static_cast<uint32_t>(g / RAW_STAGES) & 1u, guard, abort_flag,
-                         where_code(ERR_TIMEOUT_GEMM_MMA_X, rank, g)) &&
-               mbar_wait(&w16_full[c], static_cast<uint32_t>(g / CVT_STAGES) & 1u, guard, abort_flag,
-                         where_code(ERR_TIMEOUT_GEMM_MMA, rank, g));
-          if (!ok) break;
+          // a warp whose lanes disagree on whether a wait gave up may not split: it leaves by the vote below; nothing
+          // is issued or committed after such a wait, so that no slot counts as free before its copies have landed
+          ok &= mbar_wait(&x_full[s], static_cast<uint32_t>(g / RAW_STAGES) & 1u, guard, abort_flag,
+                          where_code(ERR_TIMEOUT_GEMM_MMA_X, rank, g));
+          ok &= mbar_wait(&w16_full[c], static_cast<uint32_t>(g / CVT_STAGES) & 1u, guard, abort_flag,
+                          where_code(ERR_TIMEOUT_GEMM_MMA, rank, g));
           tc_fence_after();
-          if (lane == 0) {
+          if (one && ok) {
             const uint32_t x0 = smem_u32(sX + s * X_BYTES);
             const uint32_t w0 = smem_u32(sW16 + c * W16_BYTES);
 #pragma unroll
@@ -267,11 +271,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             mma_commit_pair(&w16_empty[c], 0x3);
             if (kb + 1 == w.num_kb) mma_commit_pair(acc_full, 0x3);  // this unit's accumulators
           }
-          __syncwarp();
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           ++g;
         }
       }
-      if (lane == 0) mma_commit_pair(drain_bar, 0x3);  // all MMAs retired before either CTA frees TMEM
+      if (one) mma_commit_pair(drain_bar, 0x3);  // all MMAs retired before either CTA frees TMEM
       __syncwarp();
     }
     mbar_wait(drain_bar, 0u, guard, abort_flag, where_code(ERR_TIMEOUT_GEMM_DRAIN_MMA, rank, 0), true);
@@ -305,19 +310,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const Unit w = unit(u);
       // the epilogue boxes overlap the widened ring: no warp converts for this unit until
       // every warp has finished the previous unit's epilogue
-      if (ui > 0 && !mbar_wait(epi_done, static_cast<uint32_t>(ui - 1) & 1u, guard, abort_flag,
-                               where_code(ERR_TIMEOUT_GEMM_CONVERT, rank, 0xFFFF))) {
+      if (ui > 0 && !mbar_wait_warp(epi_done, static_cast<uint32_t>(ui - 1) & 1u, guard, abort_flag,
+                                    where_code(ERR_TIMEOUT_GEMM_CONVERT, rank, 0xFFFF))) {
         ok = false;
         break;
       }
       for (int kb = 0; kb < w.num_kb; ++kb) {
         const int s = g % RAW_STAGES;
         const int c = g % CVT_STAGES;
-        ok = mbar_wait(&w8_full[s], static_cast<uint32_t>(g / RAW_STAGES) & 1u, guard, abort_flag,
-                       where_code(ERR_TIMEOUT_GEMM_CONVERT, rank, g)) &&
-             mbar_wait(&w16_empty[c], (static_cast<uint32_t>(g / CVT_STAGES) & 1u) ^ 1u, guard, abort_flag,
-                       where_code(ERR_TIMEOUT_GEMM_CONVERT, rank, g));
-        if (!ok) break;
+        // after a wait that gave up the warp goes on, on whatever it finds and without freeing or handing over the
+        // slot; the unit's accumulators then never come, and the wait for them has the whole warp's verdict
+        const bool got = mbar_wait(&w8_full[s], static_cast<uint32_t>(g / RAW_STAGES) & 1u, guard, abort_flag,
+                                   where_code(ERR_TIMEOUT_GEMM_CONVERT, rank, g)) &
+                         mbar_wait(&w16_empty[c], (static_cast<uint32_t>(g / CVT_STAGES) & 1u) ^ 1u, guard, abort_flag,
+                                   where_code(ERR_TIMEOUT_GEMM_CONVERT, rank, g));
         // e4m3 row: 64 bytes, 64-byte swizzle (16-byte chunk j sits at chunk j ^ ((r >> 1) & 3))
         const uint8_t* src = sW8 + s * W8_BYTES + b * W8_BLOCK + r * BK;
         // widened row: 128 bytes, 128-byte swizzle (chunk j sits at chunk j ^ (r & 7))
@@ -336,13 +342,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         fence_proxy_async_smem();  // generic-proxy stores -> visible to the tensor core
         tc_fence_before();         // and the previous unit's TMEM reads ordered before its MMAs
         __syncwarp();
-        if (lane == 0) {
+        if (lane == 0 && got) {
           mbar_arrive_remote(mapa_shared(smem_u32(&w16_full[c]), 0));
           mbar_arrive(&raw_empty[s]);
         }
         ++g;
       }
-      if (!ok) break;
 
       // ---------------- epilogue of unit u: TMEM lane = token, column = channel of `acc`.
       // Per 32-channel chunk a warp reads its 32 tokens' accumulators, scales (and
@@ -369,8 +374,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       if (has_res && lane == 0) {
         for (; res_issued < min(n_early, nch); ++res_issued) issue_res(res_issued);
       }
-      if (!mbar_wait(acc_full, static_cast<uint32_t>(ui) & 1u, guard, abort_flag,
-                     where_code(ERR_TIMEOUT_GEMM_EPILOGUE, rank, ui))) {
+      if (!mbar_wait_warp(acc_full, static_cast<uint32_t>(ui) & 1u, guard, abort_flag,
+                          where_code(ERR_TIMEOUT_GEMM_EPILOGUE, rank, ui))) {
         ok = false;
         if (lane == 0) {  // no residual load left in flight
           for (int k = 0; k < res_issued; ++k) {
@@ -411,8 +416,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         if (has_res) {
           const int bx = c & 1;
-          if (!mbar_wait(&rbar[bx], (rph >> bx) & 1u, guard, abort_flag,
-                         where_code(ERR_TIMEOUT_GEMM_EPILOGUE, rank, 0x100 + c))) {
+          if (!mbar_wait_warp(&rbar[bx], (rph >> bx) & 1u, guard, abort_flag,
+                              where_code(ERR_TIMEOUT_GEMM_EPILOGUE, rank, 0x100 + c))) {
             ok = false;
             break;
           }

@@ -23,6 +23,7 @@
 #include <string.h>
 
 #include "common.cuh"
+#include "pipeline.cuh"
 
 namespace jab {
 namespace gemm8 {
@@ -140,8 +141,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       const int wr = tile_n * BN + static_cast<int>(rank) * 128;  // block b adds b * 256
       for (int kb = 0; kb < kb_total; ++kb) {
         const int s = g % STAGES;
-        if (!mbar_wait(&empty[s], (static_cast<uint32_t>(g / STAGES) & 1u) ^ 1u, guard, abort_flag,
-                       where_code(ERR_TIMEOUT_GEMM_PRODUCER, rank, g))) {
+        if (!mbar_wait_warp(&empty[s], (static_cast<uint32_t>(g / STAGES) & 1u) ^ 1u, guard, abort_flag,
+                            where_code(ERR_TIMEOUT_GEMM_PRODUCER, rank, g))) {
           ok = false;
           break;
         }
@@ -171,15 +172,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       bool ok = true;
       int g = 0, ui = 0;
       for (int u = pair; u < p.units && ok; u += pairs, ++ui) {
-        if (ui > 0 && !mbar_wait(acc_empty, static_cast<uint32_t>(ui - 1) & 1u, guard, abort_flag,
-                                 where_code(ERR_TIMEOUT_GEMM_MMA_X, rank, ui))) {
+        if (ui > 0 && !mbar_wait_warp(acc_empty, static_cast<uint32_t>(ui - 1) & 1u, guard, abort_flag,
+                                      where_code(ERR_TIMEOUT_GEMM_MMA_X, rank, ui))) {
           ok = false;
           break;
         }
         for (int kb = 0; kb < kb_total; ++kb) {
           const int s = g % STAGES;
-          if (!mbar_wait(&full[s], static_cast<uint32_t>(g / STAGES) & 1u, guard, abort_flag,
-                         where_code(ERR_TIMEOUT_GEMM_MMA, rank, g))) {
+          if (!mbar_wait_warp(&full[s], static_cast<uint32_t>(g / STAGES) & 1u, guard, abort_flag,
+                              where_code(ERR_TIMEOUT_GEMM_MMA, rank, g))) {
             ok = false;
             break;
           }
@@ -232,8 +233,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
       }
       const int row = tok_warp + lane;
       const float sa = row < p.M ? p.sa[row] : 0.f;
-      if (!mbar_wait(acc_full, static_cast<uint32_t>(ui) & 1u, guard, abort_flag,
-                     where_code(ERR_TIMEOUT_GEMM_EPILOGUE, rank, ui))) {
+      if (!mbar_wait_warp(acc_full, static_cast<uint32_t>(ui) & 1u, guard, abort_flag,
+                          where_code(ERR_TIMEOUT_GEMM_EPILOGUE, rank, ui))) {
         ok = false;
         break;
       }
