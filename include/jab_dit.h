@@ -312,10 +312,11 @@ DIT_API int dit_joint_attention(const void* qkv, void* out, int fmt, int batch, 
  *   dit_qknorm_mrope_backward   gradients of the raw q and k, and of the two gains
  *   dit_rmsnorm_rows_backward   gradient through the pre-norm, the residual's added, and of its gain
  * The gradient of a product with a frozen weight, dx = dy W for y = x W^T, is dit_gemm_w8a16 on the
- * transposed codes [K, N].  The weight's scales, one per row of W, lie on that product's contraction axis and so go
- * onto dy: with m the largest of them, pass dy * (scale / m), rounded to 16 bits, as the operand and m as the scale of
- * each of the K output channels.  (dy * scale itself, with scales of amax / 448, would lie below F16's normal
- * range: gradients of 1e-3 would keep a few bits and of 1e-4 hardly one.)
+ * transposed codes [K, N].  The weight's scales, one per row of W, lie on that product's contraction
+ * axis and so go onto dy: with m the largest of them, pass dy * (scale / m), rounded to 16 bits, as
+ * the operand and m as the scale of each of the K output channels.  (dy * scale itself, with scales
+ * of amax / 448, would lie below F16's normal range: gradients of 1e-3 would keep a few bits and of
+ * 1e-4 hardly one.)
  *
  * Row views: a pointer with a leading dimension ld (elements) is a 16-bit [batch, seq, cols] view
  * whose rows are ld apart and whose batch elements are seq * ld apart; ld >= cols, ld % 8 == 0,
@@ -326,9 +327,10 @@ DIT_API int dit_joint_attention(const void* qkv, void* out, int fmt, int batch, 
  * leading rows of each element that take part, as queries and as keys.  The rows behind them are
  * never used, whatever they hold (NaN included); their outputs and gradients are written as zeros.
  * Results do not depend on the order in which CTAs run: equal inputs give equal bits.
- * Gradients do not saturate: beyond F16's range they are infinities, and an infinity or NaN in an incoming gradient
- * reaches every gradient it enters, so that a loss scaler sees it (the forward forms saturate in F16 like the calls
- * they belong to, dit_gemm_w8a16 with y_fmt F16 among them; with y_fmt F32 or BF16 it does not).
+ * Gradients do not saturate: beyond F16's range they are infinities, and an infinity or NaN in an
+ * incoming gradient reaches every gradient it enters, so that a loss scaler sees it (the forward
+ * forms saturate in F16 like the calls they belong to, and so does dit_gemm_w8a16 with y_fmt F16;
+ * with y_fmt F32 or BF16 it does not).
  * fp32 and int32 arrays of these calls are 4-byte aligned (INVALID_ARG).
  * Each call uses its workspace until its kernels have finished; calls that may overlap (other
  * streams, captured graphs) need workspaces of their own. */

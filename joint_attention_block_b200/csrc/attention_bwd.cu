@@ -58,7 +58,8 @@ __host__ __device__ inline int blocks_of(int seq) { return (seq + T - 1) / T; }
 
 // Per (b, h), nblk = the blocks of 128 rows and one more (blocks of any R <= 128 rows end inside it):
 // nlse2 / ndelta / rows2 [B, H, nblk * 128], -log2(e) lse, -delta and (f16 only) |dO_q|^2; norms2
-// [B, H, nblk]: the block's max |dO_q|^2 and max |V_k|^2 (f16 only); tails: zero-padded copies [3: q, k, dO][B, 128, H hd] of the
+// [B, H, nblk]: the block's max |dO_q|^2 and max |V_k|^2 (f16 only); tails: zero-padded copies
+// [3: q, k, dO][B, 128, H hd] of the
 // block in which the tokens end.
 struct Workspace {
   float* nlse2;
@@ -1145,10 +1146,10 @@ __device__ __noinline__ void dq_call(uint32_t tmem, const DqMaps& tm, const BwdA
 
 // One launch for both passes: nothing is read before the wait at its start, which orders everything either
 // pass reads after the preparation and all before it, and a pair that has no more key items goes on with its
-// query items at once.  4608 x 32 heads of 128 in f16: 905 us, seven products at 1345 TFLOP/s and 1.54 GHz, the tensor
-// core busy in 72 % of the cycles.  Two launches, the second waiting for all of the first: 1100 tokens x 16 heads of 128 66 us
-// against 54, 80 tokens x 4 heads of 64 13.7 against 9.6, the padded batch of 16 heads of 64 151 against 146; 4608 x 32
-// heads of 128 852 against 861.
+// query items at once.  4608 x 32 heads of 128 in f16: 905 us, seven products at 1345 TFLOP/s and 1.54 GHz, the
+// tensor core busy in 72 % of the cycles.  Two launches, the second waiting for all of the first: 1100 tokens x
+// 16 heads of 128 66 us against 54, 80 tokens x 4 heads of 64 13.7 against 9.6, the padded batch of 16 heads of 64
+// 151 against 146; 4608 x 32 heads of 128 in bf16 852 against 861.
 template <int HD, int F>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Shared<HD>::THREADS, 1)
     bwd_kernel(const __grid_constant__ BwdMaps tm, const __grid_constant__ BwdArgs a, const KernelGuard guard) {
